@@ -65,7 +65,8 @@ const char* jamba_last_error(void);
  * -DJAMBA_CHECKS), 0 otherwise.  The checked build tests on the device every
  * index that kernels read from device data before using it: routed-row
  * positions (permutation and its inverse), expert group offsets, channel
- * permutations of the reordered caches, cache lengths of the attention step.
+ * permutations of the reordered caches, cache lengths of the attention step,
+ * page numbers and slot numbers of the paged cache.
  * A failed test latches JAMBA_ERR_BOUNDS in the device error word and skips
  * the access; nothing traps.  Group offsets are clamped into range in both
  * builds. */
@@ -581,6 +582,152 @@ jamba_status jamba_attn_step_workspace_size(const jamba_attn_config* cfg, int ba
 jamba_status jamba_attn_step(const jamba_attn_config* cfg, const jamba_attn_weights* w, const void* x,
                              const void* residual, void* out, int batch, void* k_cache, void* v_cache,
                              int max_len, int32_t* lengths, void* ws, size_t ws_bytes, jamba_stream_t stream);
+
+/* ------------------------------------------------- paged key-value cache */
+
+/* A key-value cache cut into pages of page_size tokens, so that sequences of
+ * any length share one pool, prefixes are held once by several sequences, and
+ * memory is taken and given back page by page (the serving form of the
+ * attention layer's cache; the pages say nothing about the cache's layout).
+ * All of it is device data, so every call can be captured into a CUDA graph.
+ *   data     [planes, num_pages, n_kv_heads, page_size, head_dim] dtype: the
+ *            pool.  A plane is one array of pages (for instance the keys of
+ *            layer l in plane 2l and its values in plane 2l + 1); a page
+ *            number means the same page in every plane.
+ *   refs     [num_pages] int32: how many table entries hold the page; 0 = free.
+ *            A holder outside the table (a kept prefix) may add its own count.
+ *   table    [max_seqs, max_pages] int32, row stride ld_table: entry j of
+ *            sequence s is the page of its tokens j * page_size ...  Entries
+ *            at and past ceil(lengths[s] / page_size) are not read.
+ *   lengths  [max_seqs] int32: tokens each sequence holds, the new ones of the
+ *            current call included (jamba_pages_grow makes room for them first).
+ *            0: an empty slot.
+ * Device data is not checked by the host.  A length is taken as at least 0 and at
+ * most max_pages * page_size.  A table entry outside [0, num_pages) is never
+ * used as an address: its tokens are not written, not moved and not counted, and
+ * attention reads page 0 in its place (those rows of the output are unspecified);
+ * the checked build reports it as JAMBA_ERR_BOUNDS. */
+typedef struct jamba_pages_config {
+  int num_pages;   /* pages in the pool                                   */
+  int page_size;   /* tokens per page: 16, 32, 64, 128 or 256             */
+  int n_kv_heads;  /* key/value heads                                     */
+  int head_dim;    /* 128 (the only width supported)                      */
+  int planes;      /* arrays of pages under one numbering                 */
+  int max_seqs;    /* rows of the table                                   */
+  int max_pages;   /* pages a sequence can hold                           */
+  int ld_table;    /* row stride of the table, at least max_pages         */
+  int dtype;       /* JAMBA_BF16                                          */
+} jamba_pages_config;
+
+/* Bytes of device workspace that jamba_pages_fork, _grow and _compact need
+ * (one size for all three).  The workspace carries nothing between calls. */
+jamba_status jamba_pages_workspace_size(const jamba_pages_config* cfg, size_t* bytes);
+
+/* Replaces the sequences of slots by forks of other slots, all at once:
+ *   parent [max_seqs] int32: parent[s] = s keeps slot s; parent[s] = p makes it
+ *          hold p's pages and length (as they were before the call; nothing is
+ *          copied, the pages are shared); parent[s] = -1 frees it.
+ * Pages lose the holders that slots had and gain the new ones; a page whose
+ * count reaches 0 is free.  Table entries a slot no longer holds become -1.
+ * Any other value of parent keeps the slot (checked build: JAMBA_ERR_BOUNDS).
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+jamba_status jamba_pages_fork(const jamba_pages_config* cfg, const int32_t* parent, int32_t* refs,
+                              int32_t* table, int32_t* lengths, void* ws, size_t ws_bytes, jamba_stream_t stream);
+
+/* Makes room for add[s] more tokens in every sequence and counts them into
+ * lengths: free pages are taken for the tokens past the pages held, and a last
+ * page that is partly full and shared is replaced by a copy of its own (its
+ * rows in use, in every plane), so that the new tokens touch no other
+ * sequence.  Sequences that share such a page and grow in one call take a copy
+ * each.  The lowest-numbered free pages go to the sequences in slot order.
+ *   add     [max_seqs] int32 (values below 0 count as 0)
+ *   granted [max_seqs] int32 out: 1, or 0 for a sequence that was left as it was
+ *           because it would pass max_pages, or needs pages while the pages
+ *           wanted by the slots up to it are more than the free ones
+ * Errors as jamba_pages_fork. */
+jamba_status jamba_pages_grow(const jamba_pages_config* cfg, const int32_t* add, void* data, int32_t* refs,
+                              int32_t* table, int32_t* lengths, int32_t* granted, void* ws, size_t ws_bytes,
+                              jamba_stream_t stream);
+
+/* Moves the live pages to the front of the pool: with n live pages, those
+ * numbered n and up move, in ascending order, into the free pages below n, in
+ * ascending order; rows of all planes, counts and table entries follow.
+ *   remap [num_pages] int32 out: the new number of each live page, -1 for free ones
+ * Errors as jamba_pages_fork. */
+jamba_status jamba_pages_compact(const jamba_pages_config* cfg, void* data, int32_t* refs, int32_t* table,
+                                 const int32_t* lengths, int32_t* remap, void* ws, size_t ws_bytes,
+                                 jamba_stream_t stream);
+
+/* Writes the keys and values of new tokens into their pages.  The tokens of all
+ * sequences stand one after another: sequence s has tokens q_start[s] ..
+ * q_start[s+1] - 1, the last ones of its lengths[s].
+ *   k, v  [tokens, n_kv_heads, head_dim] dtype, token stride ld_kv elements
+ *         (a multiple of 8, at least n_kv_heads * head_dim)
+ *   q_start [max_seqs + 1] int32, ascending, q_start[max_seqs] = tokens; or
+ *         NULL with tokens = max_seqs: one token for every sequence, the
+ *         empty ones (length 0) left out
+ *   k_pages, v_pages: their planes, [num_pages, n_kv_heads, page_size, head_dim]
+ * cfg->planes is not read.  Tokens that no sequence counts, or that would stand
+ * before position 0, are not written.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+jamba_status jamba_paged_append(const jamba_pages_config* cfg, const void* k, const void* v, int ld_kv,
+                                int tokens, const int32_t* q_start, void* k_pages, void* v_pages,
+                                const int32_t* table, const int32_t* lengths, jamba_stream_t stream);
+
+/* Bytes of workspace of jamba_paged_decode (tokens = max_seqs) and jamba_paged_extend. */
+jamba_status jamba_paged_decode_workspace_size(const jamba_pages_config* cfg, int n_heads, size_t* bytes);
+jamba_status jamba_paged_extend_workspace_size(const jamba_pages_config* cfg, int n_heads, int tokens,
+                                               size_t* bytes);
+
+/* Attention of one new token per sequence over its pages: query head h of
+ * sequence s over positions 0 .. lengths[s] - 1 of KV head h / (n_heads /
+ * n_kv_heads), softmax of q . k / sqrt(head_dim).
+ *   q   [max_seqs, n_heads, head_dim] dtype, token stride ld_q elements (a multiple of 8)
+ *   o   [max_seqs, n_heads, head_dim] dtype, token stride ld_o; must not overlap q
+ *   lse [max_seqs, n_heads] fp32 or NULL: log of the sum of exp of the scores, with
+ *       which attention over other keys can be joined
+ * A sequence of length 0 gets o = 0 and lse = -inf.  At most 16 query heads per
+ * KV head.  Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+jamba_status jamba_paged_decode(const jamba_pages_config* cfg, int n_heads, const void* q, int ld_q,
+                                const void* k_pages, const void* v_pages, const int32_t* table,
+                                const int32_t* lengths, void* o, int ld_o, float* lse, void* ws,
+                                size_t ws_bytes, jamba_stream_t stream);
+
+/* Causal attention of new tokens over their sequences' pages (prompts in
+ * chunks, prompts behind a shared prefix, drafted tokens, and single tokens
+ * among them): the i-th of sequence s's n tokens stands at position
+ * lengths[s] - n + i and sees the positions up to its own.
+ *   q, o, lse as in jamba_paged_decode with `tokens` rows; q_start as in
+ *   jamba_paged_append (required)
+ * A token before position 0 gets o = 0 and lse = -inf; rows of q past
+ * q_start[max_seqs] are left out.  At most 128 query heads per KV head.
+ * Errors as jamba_paged_decode. */
+jamba_status jamba_paged_extend(const jamba_pages_config* cfg, int n_heads, const void* q, int ld_q, int tokens,
+                                const int32_t* q_start, const void* k_pages, const void* v_pages,
+                                const int32_t* table, const int32_t* lengths, void* o, int ld_o, float* lse,
+                                void* ws, size_t ws_bytes, jamba_stream_t stream);
+
+/* The attention layer over the paged cache: fused q|k|v projection, append,
+ * attention, out_proj (+ residual).  pages->n_kv_heads and head_dim are the
+ * layer's; lengths already count the new tokens (jamba_pages_grow).
+ * prefill: x, residual, out [tokens, d_model], ragged as in jamba_paged_extend;
+ *   a row that no sequence counts attends to nothing (its output is the residual, or 0).
+ * step: one token for every slot, x, residual, out [max_seqs, d_model]; slots of length 0
+ *   write nothing and attend to nothing (their output is the residual, or 0).
+ *   At most 16 query heads per KV head.
+ * Errors: INVALID_ARG (out may not alias x), UNSUPPORTED, WORKSPACE, CUDA. */
+jamba_status jamba_attn_paged_prefill_workspace_size(const jamba_attn_config* cfg, const jamba_pages_config* pages,
+                                                     int tokens, size_t* bytes);
+jamba_status jamba_attn_paged_prefill(const jamba_attn_config* cfg, const jamba_attn_weights* w,
+                                      const jamba_pages_config* pages, const void* x, const void* residual,
+                                      void* out, int tokens, const int32_t* q_start, void* k_pages, void* v_pages,
+                                      const int32_t* table, const int32_t* lengths, void* ws, size_t ws_bytes,
+                                      jamba_stream_t stream);
+jamba_status jamba_attn_paged_step_workspace_size(const jamba_attn_config* cfg, const jamba_pages_config* pages,
+                                                  size_t* bytes);
+jamba_status jamba_attn_paged_step(const jamba_attn_config* cfg, const jamba_attn_weights* w,
+                                   const jamba_pages_config* pages, const void* x, const void* residual, void* out,
+                                   void* k_pages, void* v_pages, const int32_t* table, const int32_t* lengths,
+                                   void* ws, size_t ws_bytes, jamba_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -60,6 +60,11 @@ class AttnWeights(ctypes.Structure):
     _fields_ = [("w_qkv", ctypes.c_void_p), ("w_o", ctypes.c_void_p)]
 
 
+class PagesConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("num_pages", "page_size", "n_kv_heads", "head_dim", "planes",
+                                            "max_seqs", "max_pages", "ld_table", "dtype")]
+
+
 P = ctypes.c_void_p
 I = ctypes.c_int
 SZ = ctypes.c_size_t
@@ -107,6 +112,19 @@ SIGNATURES = {
     "jamba_attn_step_workspace_size": [ctypes.POINTER(AttnConfig), I, I, ctypes.POINTER(SZ)],
     "jamba_attn_step": [ctypes.POINTER(AttnConfig), ctypes.POINTER(AttnWeights), P, P, P, I, P, P, I, P,
                         P, SZ, P],
+    "jamba_pages_workspace_size": [P, ctypes.POINTER(SZ)],
+    "jamba_pages_fork": [P, P, P, P, P, P, SZ, P],
+    "jamba_pages_grow": [P, P, P, P, P, P, P, P, SZ, P],
+    "jamba_pages_compact": [P, P, P, P, P, P, P, SZ, P],
+    "jamba_paged_append": [P, P, P, I, I, P, P, P, P, P, P],
+    "jamba_paged_decode_workspace_size": [P, I, ctypes.POINTER(SZ)],
+    "jamba_paged_extend_workspace_size": [P, I, I, ctypes.POINTER(SZ)],
+    "jamba_paged_decode": [P, I, P, I, P, P, P, P, P, I, P, P, SZ, P],
+    "jamba_paged_extend": [P, I, P, I, I, P, P, P, P, P, P, I, P, P, SZ, P],
+    "jamba_attn_paged_prefill_workspace_size": [P, P, I, ctypes.POINTER(SZ)],
+    "jamba_attn_paged_prefill": [P, P, P, P, P, P, I, P, P, P, P, P, P, SZ, P],
+    "jamba_attn_paged_step_workspace_size": [P, P, ctypes.POINTER(SZ)],
+    "jamba_attn_paged_step": [P, P, P, P, P, P, P, P, P, P, P, SZ, P],
 }
 
 _lib = None

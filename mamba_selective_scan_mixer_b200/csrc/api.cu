@@ -8,6 +8,7 @@
 #include <string>
 #include <vector>
 
+#include "api.hpp"
 #include "gemm_tc.cuh"
 #include "host.hpp"
 
@@ -36,24 +37,7 @@ struct jamba_mamba {
 
 namespace {
 
-constexpr size_t kAlign = 256;
-inline size_t al(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-
-// Sequential carve-out of a workspace; with a null base it only measures.
-struct Carver {
-  uint8_t* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base(reinterpret_cast<uint8_t*>(b)) {}
-  template <typename T = void>
-  T* take(size_t bytes) {
-    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
-    off += al(bytes);
-    return p;
-  }
-};
-
 inline int esize(int dtype) { return dtype == JAMBA_BF16 ? 2 : 4; }
-inline cudaStream_t cs(jamba_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 struct PrefillWs {
   void* xz; void* xc; float* xpart; void* dtlow; float* bc; float* dt; void* y; float* conv_tmp; void* scan;
@@ -141,26 +125,12 @@ StepWs carve_step(const jamba_mamba_config& c, int batch, void* ws) {
   return p;
 }
 
-GemmDesc gdesc(const void* a, long long lda, const void* b, long long ldb, int M, int N, int K, int epi, void* out,
-               long long ldo) {
-  GemmDesc g = {};
-  g.a = a; g.lda = lda; g.b = b; g.ldb = ldb; g.M = M; g.N = N; g.K = K; g.epi = epi; g.out = out; g.ldo = ldo;
-  g.splits = 1;
-  return g;
-}
-
 jamba_status gemm_any(int dtype, const GemmDesc& g, cudaStream_t s) {
   return dtype == JAMBA_BF16 ? gemm_bf16(g, s) : gemm_f32(g, s);
 }
 
 jamba_status check_dtype(int d) {
   return (d == JAMBA_BF16 || d == JAMBA_F32) ? JAMBA_OK : fail(JAMBA_ERR_UNSUPPORTED, "dtype must be JAMBA_F32 or JAMBA_BF16");
-}
-
-jamba_status check_ptr(const void* p, const char* name, bool required = true) {
-  if (!p) return required ? fail(JAMBA_ERR_INVALID_ARG, std::string(name) + " is null") : JAMBA_OK;
-  if (!aligned16(p)) return fail(JAMBA_ERR_INVALID_ARG, std::string(name) + " is not 16-byte aligned");
-  return JAMBA_OK;
 }
 
 jamba_status check_device(const jamba_mamba* h) {
@@ -1328,7 +1298,9 @@ AttnStepWs carve_attn_step(const jamba_attn_config& c, int B, int max_len, void*
   a.total = cv.off;
   return a;
 }
-jamba_status check_attn_cfg(const jamba_attn_config* c) {
+}  // namespace
+
+jamba_status jb::check_attn_cfg(const jamba_attn_config* c) {
   if (!c) return fail(JAMBA_ERR_INVALID_ARG, "attention: null config");
   if (c->dtype != JAMBA_BF16) return fail(JAMBA_ERR_UNSUPPORTED, "attention: bf16 only");
   if (c->head_dim != 128) return fail(JAMBA_ERR_UNSUPPORTED, "attention: head_dim must be 128");
@@ -1337,7 +1309,6 @@ jamba_status check_attn_cfg(const jamba_attn_config* c) {
   if (c->d_model <= 0 || c->d_model % 64) return fail(JAMBA_ERR_UNSUPPORTED, "attention: d_model must be a multiple of 64");
   return JAMBA_OK;
 }
-}  // namespace
 
 extern "C" {
 

@@ -232,4 +232,22 @@ int attn_decode_splits(int B, int G, int max_len);
 jamba_status attn_decode_core(const void* qkv, void* k_cache, void* v_cache, int max_len, int* lengths, float* part,
                               int splits, void* o, int B, int H, int G, cudaStream_t s);
 
+// ---------------------------------------------------------------- paged key-value cache
+struct PageGeom;   // pages.cuh
+size_t pages_workspace_bytes(const PageGeom& g);
+jamba_status pages_fork(const PageGeom& g, const int* parent, int* refs, int* table, int* lengths, void* ws,
+                        cudaStream_t s);
+jamba_status pages_grow(const PageGeom& g, const int* add, void* data, int* refs, int* table, int* lengths,
+                        int* granted, void* ws, cudaStream_t s);
+jamba_status pages_compact(const PageGeom& g, void* data, int* refs, int* table, const int* lengths, int* remap,
+                           void* ws, cudaStream_t s);
+jamba_status paged_append(const PageGeom& g, const void* k, const void* v, int ld, int tokens, const int* q_start,
+                          void* k_pages, void* v_pages, const int* table, const int* lengths, cudaStream_t s);
+// H query heads over g.G KV heads; q_start null: one token per sequence (tokens = g.S).
+// Rows of o that no sequence counts are left as they are, or zeroed with fill.
+size_t paged_attn_workspace_bytes(const PageGeom& g, int H, int tokens, bool ragged);
+jamba_status paged_attn(const PageGeom& g, int H, const void* q, long long ld_q, int tokens, const int* q_start,
+                        const void* k_pages, const void* v_pages, const int* table, const int* lengths, void* o,
+                        long long ld_o, float* lse, bool fill, void* ws, cudaStream_t s);
+
 }  // namespace jb

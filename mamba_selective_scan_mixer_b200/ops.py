@@ -7,7 +7,7 @@ import ctypes
 
 import torch
 
-from . import _abi
+from . import _abi, paged
 from ._abi import check, lib
 
 _DT = {torch.bfloat16: _abi.JAMBA_BF16, torch.float32: _abi.JAMBA_F32}
@@ -457,6 +457,52 @@ class Attention:
                                     _p(k_cache), _p(v_cache), max_len, _p(lengths), _p(ws), ws.numel(),
                                     _stream(stream)))
         return out
+
+    def _paged(self, x, cache, layer, tokens, q_start, residual, out, stream):
+        if self.shape.n_kv_heads != cache.data.shape[2]:
+            raise ValueError("the cache holds %d KV heads" % cache.data.shape[2])
+        named = [("x", x), ("w_o", self.w_o)] + [(n, t) for n, t in (("residual", residual), ("out", out),
+                                                                   ("q_start", q_start)) if t is not None]
+        paged._same_device(cache.data, named)
+        for t, name in ((x, "x"), (residual, "residual"), (out, "out")):
+            _contig(t, name)
+            if t is not None and (tuple(t.shape) != (tokens, self.shape.d_model) or t.dtype != self.w_o.dtype):
+                raise ValueError("%s must be %s [%d, %d]" % (name, self.w_o.dtype, tokens, self.shape.d_model))
+        cfg, k, v = cache.config(layer)
+        n = ctypes.c_size_t()
+        L, a, p = lib(), ctypes.byref(self.cfg), ctypes.byref(cfg)
+        with paged._Call(cache.data.device, stream) as st:
+            out = torch.empty_like(x) if out is None else out
+            if tokens == 0:
+                return out
+            if q_start is None:
+                check(L.jamba_attn_paged_step_workspace_size(a, p, ctypes.byref(n)))
+            else:
+                check(L.jamba_attn_paged_prefill_workspace_size(a, p, tokens, ctypes.byref(n)))
+            ws = torch.empty(n.value, dtype=torch.uint8, device=x.device)
+            if q_start is None:
+                check(L.jamba_attn_paged_step(a, ctypes.byref(self.w), p, _p(x), _p(residual), _p(out), _p(k), _p(v),
+                                              _p(cache.table), _p(cache.lengths), _p(ws), ws.numel(), st))
+            else:
+                check(L.jamba_attn_paged_prefill(a, ctypes.byref(self.w), p, _p(x), _p(residual), _p(out), tokens,
+                                                 _p(q_start), _p(k), _p(v), _p(cache.table), _p(cache.lengths),
+                                                 _p(ws), ws.numel(), st))
+        return out
+
+    def paged_prefill(self, x, q_start, cache, layer=0, residual=None, out=None, stream=None):
+        """x [tokens, d_model], the new tokens of all slots of a PagedKVCache one
+        after another (rows q_start[s] .. q_start[s+1] - 1 are slot s's; the
+        cache's lengths count them, see its grow): appends their keys and values to
+        the layer's pages and attends causally over everything each slot holds."""
+        if x.dim() != 2:
+            raise ValueError("x must be [tokens, d_model]")
+        paged._ints(q_start, "q_start", (cache.table.shape[0] + 1,))
+        return self._paged(x, cache, layer, x.shape[0], q_start, residual, out, stream)
+
+    def paged_step(self, x, cache, layer=0, residual=None, out=None, stream=None):
+        """x [max_seqs, d_model], one new token for every slot (empty slots are
+        left out; the cache's lengths count the new tokens)."""
+        return self._paged(x, cache, layer, cache.table.shape[0], None, residual, out, stream)
 
 
 def layer_pair(mixer, moe, x, g1, g2, eps=1e-6, stream=None):
