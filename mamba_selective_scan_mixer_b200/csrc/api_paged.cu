@@ -90,7 +90,6 @@ jamba_status check_attn_args(int n_heads, const void* q, int ld_q, const void* k
 
 struct PagedLayerWs {
   void *qkv, *attn, *o; float* opart;
-  size_t attn_bytes;
   int o_splits;
   size_t total;
 };
@@ -101,8 +100,7 @@ PagedLayerWs carve_layer(const jamba_attn_config& c, const PageGeom& g, int toke
   Carver cv(ws);
   a.qkv = cv.take((size_t)tokens * W * 2);
   a.o = cv.take((size_t)tokens * HD * 2);
-  a.attn_bytes = paged_attn_workspace_bytes(g, c.n_heads, tokens, ragged);
-  a.attn = cv.take(a.attn_bytes);
+  a.attn = cv.take(ragged ? paged_extend_workspace_bytes() : paged_decode_workspace_bytes(g, c.n_heads));
   a.opart = ragged ? nullptr : cv.take<float>((size_t)a.o_splits * tokens * c.d_model * 4);
   a.total = cv.off;
   return a;
@@ -214,7 +212,7 @@ jamba_status jamba_paged_decode_workspace_size(const jamba_pages_config* cfg, in
   JB_TRY(geom(cfg, &g));
   JB_TRY(check_heads(g, n_heads, g.S, DECODE_MAX_REP));
   if (!bytes) return fail(JAMBA_ERR_INVALID_ARG, "paged decode workspace: bytes is null");
-  *bytes = paged_attn_workspace_bytes(g, n_heads, g.S, false);
+  *bytes = paged_decode_workspace_bytes(g, n_heads);
   return JAMBA_OK;
 }
 
@@ -224,7 +222,7 @@ jamba_status jamba_paged_extend_workspace_size(const jamba_pages_config* cfg, in
   if (tokens < 0) return fail(JAMBA_ERR_INVALID_ARG, "paged extend workspace: negative tokens");
   JB_TRY(check_heads(g, n_heads, tokens, EXTEND_MAX_REP));
   if (!bytes) return fail(JAMBA_ERR_INVALID_ARG, "paged extend workspace: bytes is null");
-  *bytes = paged_attn_workspace_bytes(g, n_heads, tokens, true);
+  *bytes = paged_extend_workspace_bytes();
   return JAMBA_OK;
 }
 
@@ -237,10 +235,10 @@ jamba_status jamba_paged_decode(const jamba_pages_config* cfg, int n_heads, cons
   JB_TRY(geom(cfg, &g));
   JB_TRY(check_heads(g, n_heads, g.S, DECODE_MAX_REP));
   JB_TRY(check_attn_args(n_heads, q, ld_q, k_pages, v_pages, table, lengths, o, ld_o, lse, ws));
-  if (ws_bytes < paged_attn_workspace_bytes(g, n_heads, g.S, false))
+  if (ws_bytes < paged_decode_workspace_bytes(g, n_heads))
     return fail(JAMBA_ERR_WORKSPACE, "paged decode: workspace too small");
   JB_TRY(ready());
-  return paged_attn(g, n_heads, q, ld_q, g.S, nullptr, k_pages, v_pages, table, lengths, o, ld_o, lse, false, ws, cs(stream));
+  return paged_decode(g, n_heads, q, ld_q, k_pages, v_pages, table, lengths, o, ld_o, lse, ws, cs(stream));
 }
 
 jamba_status jamba_paged_extend(const jamba_pages_config* cfg, int n_heads, const void* q, int ld_q, int tokens,
@@ -254,12 +252,12 @@ jamba_status jamba_paged_extend(const jamba_pages_config* cfg, int n_heads, cons
   JB_TRY(check_heads(g, n_heads, tokens, EXTEND_MAX_REP));
   JB_TRY(check_int(q_start, "q_start"));
   JB_TRY(check_attn_args(n_heads, q, ld_q, k_pages, v_pages, table, lengths, o, ld_o, lse, ws));
-  if (ws_bytes < paged_attn_workspace_bytes(g, n_heads, tokens, true))
+  if (ws_bytes < paged_extend_workspace_bytes())
     return fail(JAMBA_ERR_WORKSPACE, "paged extend: workspace too small");
   if (tokens == 0) return JAMBA_OK;
   JB_TRY(ready());
-  return paged_attn(g, n_heads, q, ld_q, tokens, q_start, k_pages, v_pages, table, lengths, o, ld_o, lse, false,
-                    ws, cs(stream));
+  return paged_extend(g, n_heads, q, ld_q, tokens, q_start, k_pages, v_pages, table, lengths, o, ld_o, lse, false, ws,
+                      cs(stream));
 }
 
 jamba_status jamba_attn_paged_prefill_workspace_size(const jamba_attn_config* cfg, const jamba_pages_config* pages,
@@ -291,8 +289,8 @@ jamba_status jamba_attn_paged_prefill(const jamba_attn_config* cfg, const jamba_
   bf16* qkv = reinterpret_cast<bf16*>(a.qkv);
   JB_TRY(gemm_bf16(gdesc(x, dm, w->w_qkv, dm, tokens, W, dm, EPI_BF16, qkv, W), s));
   JB_TRY(paged_append(g, qkv + HD, qkv + HD + KD, W, tokens, q_start, k_pages, v_pages, table, lengths, s));
-  JB_TRY(paged_attn(g, c.n_heads, qkv, W, tokens, q_start, k_pages, v_pages, table, lengths, a.o, HD, nullptr, true,
-                    a.attn, s));
+  JB_TRY(paged_extend(g, c.n_heads, qkv, W, tokens, q_start, k_pages, v_pages, table, lengths, a.o, HD, nullptr, true,
+                      a.attn, s));
   GemmDesc go = gdesc(a.o, HD, w->w_o, HD, tokens, dm, HD, EPI_BF16, out, dm);
   go.residual = residual;
   go.ldr = dm;
@@ -331,7 +329,7 @@ jamba_status jamba_attn_paged_step(const jamba_attn_config* cfg, const jamba_att
   g1.bn = 64;
   JB_TRY(gemm_bf16(g1, s));
   JB_TRY(paged_append(g, qkv + HD, qkv + HD + KD, W, B, nullptr, k_pages, v_pages, table, lengths, s));
-  JB_TRY(paged_attn(g, c.n_heads, qkv, W, B, nullptr, k_pages, v_pages, table, lengths, a.o, HD, nullptr, true, a.attn, s));
+  JB_TRY(paged_decode(g, c.n_heads, qkv, W, k_pages, v_pages, table, lengths, a.o, HD, nullptr, a.attn, s));
   GemmDesc g2 = gdesc(w->w_o, HD, a.o, HD, dm, B, HD, EPI_F32, a.opart, dm);
   g2.transpose_out = 1;
   g2.bn = 64;

@@ -243,11 +243,15 @@ jamba_status pages_compact(const PageGeom& g, void* data, int* refs, int* table,
                            void* ws, cudaStream_t s);
 jamba_status paged_append(const PageGeom& g, const void* k, const void* v, int ld, int tokens, const int* q_start,
                           void* k_pages, void* v_pages, const int* table, const int* lengths, cudaStream_t s);
-// H query heads over g.G KV heads; q_start null: one token per sequence (tokens = g.S).
-// Rows of o that no sequence counts are left as they are, or zeroed with fill.
-size_t paged_attn_workspace_bytes(const PageGeom& g, int H, int tokens, bool ragged);
-jamba_status paged_attn(const PageGeom& g, int H, const void* q, long long ld_q, int tokens, const int* q_start,
-                        const void* k_pages, const void* v_pages, const int* table, const int* lengths, void* o,
-                        long long ld_o, float* lse, bool fill, void* ws, cudaStream_t s);
+// H query heads over g.G KV heads; one new token of every sequence
+size_t paged_decode_workspace_bytes(const PageGeom& g, int H);
+jamba_status paged_decode(const PageGeom& g, int H, const void* q, long long ld_q, const void* k_pages,
+                          const void* v_pages, const int* table, const int* lengths, void* o, long long ld_o,
+                          float* lse, void* ws, cudaStream_t s);
+// ... a ragged batch of new tokens; rows of o that no sequence counts are left as they are, or zeroed with fill
+size_t paged_extend_workspace_bytes();
+jamba_status paged_extend(const PageGeom& g, int H, const void* q, long long ld_q, int tokens, const int* q_start,
+                          const void* k_pages, const void* v_pages, const int* table, const int* lengths, void* o,
+                          long long ld_o, float* lse, bool fill, void* ws, cudaStream_t s);
 
 }  // namespace jb

@@ -1,11 +1,10 @@
-// Attention over the paged key-value cache: one new token per sequence
-// (decode) or a ragged batch of new tokens (extend), causal, grouped query heads.
-//
-//   o_t = sum_j softmax_j(q_t . k_j / sqrt(d)) v_j over the positions j <= pos(t),
-//   lse_t = log sum_j exp(q_t . k_j / sqrt(d)),
+// Attention of one new token per sequence over the paged key-value cache, grouped
+// query heads:
+//   o = sum_j softmax_j(q . k_j / sqrt(d)) v_j over the sequence's positions,
+//   lse = log sum_j exp(q . k_j / sqrt(d)),
 // in one pass over the keys with a running maximum and sum.
 //
-// A CTA takes one token, up to eight query heads of one KV head and a part of
+// A CTA takes one sequence, up to eight query heads of one KV head and a part of
 // the positions; the partial softmaxes of the parts are joined by a second kernel.
 #include "host.hpp"
 #include "pages.cuh"
@@ -35,32 +34,20 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 
 struct PagedAttnParams {
   PageGeom g;
-  int H, rep, tokens;
+  int H, rep;
   const bf16* q; long long ld_q;
-  const int* q_start;              // null: token t is sequence t's last one
   const bf16 *k, *v;
   const int *table, *lengths;
   bf16* o; long long ld_o;
   float* lse;
   float sl2;                       // log2(e) / sqrt(head_dim)
   float* part;                     // [tokens * H][splits][D + 2]
-  int splits, fill;
+  int splits;
   int* err;
 };
 
-// the sequence of token t and the number of positions it sees
-__device__ __forceinline__ void token_view(const PagedAttnParams& p, int t, int& s, int& n) {
-  s = p.q_start ? token_seq(p.q_start, p.g.S, t) : t;
-  n = 0;
-  if (s >= 0) {
-    const int len = clamp_len(p.g, p.lengths[s], p.err);
-    n = p.q_start ? min(len, len - p.q_start[s + 1] + t + 1) : len;
-    if (n < 0) n = 0;
-  }
-}
-
 __global__ void __launch_bounds__(128)
-paged_rows_kernel(const PagedAttnParams p) {
+paged_decode_kernel(const PagedAttnParams p) {
   extern __shared__ uint8_t dsm[];
   __shared__ float w_m[4][ROW_REP], w_l[4][ROW_REP];
   __shared__ float w_o[4][ROW_REP][PG_D];
@@ -72,8 +59,7 @@ paged_rows_kernel(const PagedAttnParams p) {
   const int head0 = g * p.rep + hg * ROW_REP;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, tq = lane & 3;   // mma fragment coordinates
-  int s, n;
-  token_view(p, t, s, n);
+  const int n = clamp_len(p.g, p.lengths[t], p.err);
   const int per = (n + p.splits - 1) / p.splits;
   const int p0 = min(n, split * per), p1 = min(n, p0 + per);
   uint32_t qb[8][2];                          // B fragments of Q^T
@@ -90,7 +76,7 @@ paged_rows_kernel(const PagedAttnParams p) {
       qb[kk][1] = hi;
     }
   }
-  const int* trow = p.table + (long long)(s < 0 ? 0 : s) * p.g.ld_table;
+  const int* trow = p.table + (long long)t * p.g.ld_table;
   const uint32_t wbase = smem_u32(dsm) + warp * 2 * 2 * ROW_TILE;
   // stage 16 rows of K and V at positions c0.. (within one page) into buffer `buf`, zeros past p1
   auto stage = [&](int c0, int buf) {
@@ -213,11 +199,10 @@ paged_rows_kernel(const PagedAttnParams p) {
 
 // joins the parts of (token, head): o = sum of o_i 2^(m_i - m) / sum of l_i 2^(m_i - m)
 __global__ void __launch_bounds__(128)
-paged_join_kernel(const PagedAttnParams p) {
+paged_decode_join_kernel(const PagedAttnParams p) {
   griddep_wait();
   griddep_launch();
   const int t = blockIdx.x / p.H, h = blockIdx.x % p.H, d = threadIdx.x;
-  if (!p.fill && p.q_start && token_seq(p.q_start, p.g.S, t) < 0) return;   // a row that no sequence counts
   const float* src = p.part + (long long)blockIdx.x * p.splits * (PG_D + 2);
   float mm = -INFINITY;
   for (int s = 0; s < p.splits; ++s) mm = fmaxf(mm, src[s * (PG_D + 2) + PG_D]);
@@ -242,21 +227,20 @@ static int row_splits(const PageGeom& g, int H, int tokens) {
   return s < 1 ? 1 : (int)s;
 }
 
-size_t paged_attn_workspace_bytes(const PageGeom& g, int H, int tokens, bool) {
-  return (size_t)tokens * H * row_splits(g, H, tokens) * (PG_D + 2) * 4;
+size_t paged_decode_workspace_bytes(const PageGeom& g, int H) {
+  return (size_t)g.S * H * row_splits(g, H, g.S) * (PG_D + 2) * 4;
 }
 
-jamba_status paged_attn(const PageGeom& g, int H, const void* q, long long ld_q, int tokens, const int* q_start,
-                        const void* k_pages, const void* v_pages, const int* table, const int* lengths, void* o,
-                        long long ld_o, float* lse, bool fill, void* ws, cudaStream_t s) {
+jamba_status paged_decode(const PageGeom& g, int H, const void* q, long long ld_q, const void* k_pages,
+                          const void* v_pages, const int* table, const int* lengths, void* o, long long ld_o,
+                          float* lse, void* ws, cudaStream_t s) {
+  const int tokens = g.S;
   PagedAttnParams p;
   p.g = g;
   p.H = H;
   p.rep = H / g.G;
-  p.tokens = tokens;
   p.q = reinterpret_cast<const bf16*>(q);
   p.ld_q = ld_q;
-  p.q_start = q_start;
   p.k = reinterpret_cast<const bf16*>(k_pages);
   p.v = reinterpret_cast<const bf16*>(v_pages);
   p.table = table;
@@ -267,18 +251,17 @@ jamba_status paged_attn(const PageGeom& g, int H, const void* q, long long ld_q,
   p.sl2 = 1.4426950408889634f / sqrtf((float)PG_D);
   p.part = reinterpret_cast<float*>(ws);
   p.splits = row_splits(g, H, tokens);
-  p.fill = fill;
   p.err = device_error_word();
   const int hgs = (p.rep + ROW_REP - 1) / ROW_REP;
   static std::atomic<bool> configured[64];
   int dev = 0;
   JB_CUDA(cudaGetDevice(&dev));
   if (dev < 64 && !configured[dev]) {
-    JB_CUDA(cudaFuncSetAttribute(paged_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ROW_SMEM));
+    JB_CUDA(cudaFuncSetAttribute(paged_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ROW_SMEM));
     configured[dev] = true;
   }
-  JB_CUDA(launch_pdl(paged_rows_kernel, dim3((unsigned)(tokens * g.G * hgs), p.splits), dim3(128), ROW_SMEM, s, p));
-  JB_CUDA(launch_pdl(paged_join_kernel, dim3((unsigned)(tokens * H)), dim3(PG_D), 0, s, p));
+  JB_CUDA(launch_pdl(paged_decode_kernel, dim3((unsigned)(tokens * g.G * hgs), p.splits), dim3(128), ROW_SMEM, s, p));
+  JB_CUDA(launch_pdl(paged_decode_join_kernel, dim3((unsigned)(tokens * H)), dim3(PG_D), 0, s, p));
   return JAMBA_OK;
 }
 
