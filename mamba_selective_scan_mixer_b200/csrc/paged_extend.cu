@@ -33,8 +33,9 @@ namespace jb {
 
 constexpr int EX_BK = 128;                       // keys per block
 constexpr int EX_SLOTS = 5;                      // ring of K and V blocks
-constexpr int EX_THREADS = 384;                  // producer, MMA, two idle warps, 4 + 4 softmax warps
-constexpr int EX_MIN_BLOCKS = 2;                 // of a CTA's range
+constexpr int EX_THREADS = 640;                  // producer, an MMA warp per tile, V tails, 8 + 8 softmax warps
+constexpr int EX_MIN_COST = 4;                   // of a CTA's range
+constexpr int EX_UNIT_COST = 2;                  // what a unit costs beyond its blocks (Q, first maximum, output), in blocks
 
 struct ExSmem {
   static constexpr uint32_t SUB = 128 * 128;     // 128 rows x 64 bf16, swizzled
@@ -98,13 +99,13 @@ struct ExSeq {
     const int seen = len - n + min(n, (u + 1) * 2 * p.tpt);
     return seen <= EX_BK ? 1 : (seen + EX_BK - 1) / EX_BK;
   }
-  // blocks of the units before u (of one KV head)
+  // cost of the units before u (of one KV head)
   __device__ long long before(const ExParams& p, int u) const {
     const long long tc = 2 * p.tpt, base = len - n;
     if (u <= 0) return 0;
-    long long last = 0;
+    long long last = (long long)EX_UNIT_COST * u;
     if (u == units) {                            // the last unit may be short
-      last = blocks(p, units - 1);
+      last += blocks(p, units - 1);
       --u;
     }
     // units 0 .. u-1 end at base + (i + 1) tc: ceil(x / 128) = floor((x + 127) / 128), 1 where x <= 0
@@ -118,21 +119,23 @@ struct ExSeq {
   __device__ long long total(const ExParams& p) const { return units ? before(p, units) * p.g.G : 0; }
 };
 
-// One stretch of blocks [kb0, kb1) of unit (s, g, u); every role walks the same items.
+// One stretch of blocks [kb0, kb1) of unit (s, g, u); every role walks the same items.  Ranges are
+// cut by cost: a unit is EX_UNIT_COST steps without a block, then a step per block.
 struct ExWalk {
   ExSeq q;
   int s, g, u, kb0, kb1, nb;                     // nb: blocks of the unit
-  long long left;                                // blocks of the CTA's range from kb0 on
-  __device__ bool open(const ExParams& p) {      // the item at (s, g, u, kb0)
+  long long at, left;                            // step of the unit that the item starts at; steps of the range from there on
+  __device__ bool open(const ExParams& p) {      // the item at (s, g, u, at); false: no block is left
     if (left <= 0) return false;
     nb = q.blocks(p, u);
-    kb1 = (int)min((long long)nb, kb0 + left);
-    return true;
+    kb0 = max(0, (int)at - EX_UNIT_COST);
+    kb1 = max(0, (int)min((long long)nb, at + left - EX_UNIT_COST));
+    return kb1 > kb0;
   }
   __device__ bool next(const ExParams& p) {
-    left -= kb1 - kb0;
+    left -= EX_UNIT_COST + nb - at;
     if (left <= 0) return false;
-    kb0 = 0;
+    at = 0;
     if (++u == q.units) {
       u = 0;
       if (++g == p.g.G) {
@@ -150,7 +153,168 @@ struct ExWalk {
   }
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+constexpr float EX_RAISE = 8.f;    // log2 units: the reference is raised when a maximum passes it by more
+constexpr float EX_REDO = 64.f;    // ... and the block is formed again when by more than this
+
+// Softmax warps hold 16 rows of a tile each: in tcgen05.ld / st .16x256b and .16x128b a row's columns
+// lie over the four lanes of a quad (lane i: rows i / 4 and i / 4 + 8; of each 8 columns of 32
+// bits numbers 2 (i % 4) and the next; of each 4 columns of packed bf16 number i % 4), so a thread
+// has 32 scores of two rows, and a row's maximum and sum are two shuffles away.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, float (&v)[16]) {   // 32 columns
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b(uint32_t taddr, const float (&v)[16]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, const uint32_t (&r)[32]) {   // 64 columns
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// waits for the loads so far, tied to the registers of one (see tmem_wait_ld32)
+__device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+// column of register k of 32-column chunk c in a .16x256b load; its row is k & 2 (0: lane / 4, 2: + 8)
+__device__ __forceinline__ int chunk_col(int c, int k, int quad) { return 32 * c + 8 * (k >> 2) + 2 * quad + (k & 1); }
+
+// the largest score of the thread's two rows in one block (raw, before the scale), keys past lim left out when masked
+__device__ __forceinline__ void ex_row_max(uint32_t tS, bool masked, const int (&lim)[2], int quad, float (&mx)[2]) {
+  mx[0] = mx[1] = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float v[16];
+    tmem_ld_16x256b(tS + 32 * c, v);
+    tmem_wait_ld16(v);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int e = (k >> 1) & 1;
+      mx[e] = fmaxf(mx[e], masked && chunk_col(c, k, quad) > lim[e] ? -INFINITY : v[k]);
+    }
+  }
+  mx[0] = quad_max(mx[0]);
+  mx[1] = quad_max(mx[1]);
+}
+
+constexpr int EX_FMA_EVERY = 4;    // of the pairs of terms, one in so many goes to ex2_fma
+constexpr float EXC0 = 0.99999926144f, EXC1 = 0.69312181475f, EXC2 = 0.24024744849f, EXC3 = 0.05591786025f,
+                EXC4 = 0.00957010107f;
+
+// 2^x for both halves on the FMA pipe, x in [-126, 126] (lower ones count as -126): the nearest
+// integer n through the mantissa of x + 1.5 2^23, a degree-4 polynomial for 2^f with f = x - n in
+// [-1/2, 1/2] (fitted for the least largest
+// relative error, 2.6e-6; P keeps 2^-9), and n
+// added to its exponent.  Takes some of the terms because ex2 alone runs at 16 a cycle and SM: 128 x 256
+// terms take the 2048 cycles that their four products take.
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+  const float big = 12582912.f;
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 one = make_float2(1.f, 1.f);
+  const float2 t = ffma2(x, one, make_float2(big, big));
+  const float2 n = ffma2(t, one, make_float2(-big, -big));
+  const float2 f = ffma2(n, make_float2(-1.f, -1.f), x);
+  float2 y = make_float2(EXC4, EXC4);
+  y = ffma2(y, f, make_float2(EXC3, EXC3));
+  y = ffma2(y, f, make_float2(EXC2, EXC2));
+  y = ffma2(y, f, make_float2(EXC1, EXC1));
+  y = ffma2(y, f, make_float2(EXC0, EXC0));
+  return make_float2(__int_as_float(__float_as_int(y.x) + (__float_as_int(t.x) << 23)),
+                     __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
+}
+
+// The terms 2^(s sl2 + ref) of the thread's two rows in bf16 pairs, their sums (before rounding, the thread's own
+// columns only) and the rows' largest scores.
+template <bool MASKED>
+__device__ __forceinline__ void ex_terms_t(uint32_t tS, const int (&lim)[2], int quad, const float (&ref)[2], float sl2,
+                                           uint32_t (&pk)[32], float (&mx)[2], float (&sum)[2]) {
+  const float2 sl = make_float2(sl2, sl2);
+  float2 sm[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  mx[0] = mx[1] = -INFINITY;
+  float s[2][16];
+  tmem_ld_16x256b(tS, s[0]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float(&v)[16] = s[c & 1];
+    tmem_wait_ld16(v);
+    if (c < 3) tmem_ld_16x256b(tS + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {                // pairs of columns: group i / 2, row i % 2
+      const int e = i & 1;
+      float a = v[2 * i], b = v[2 * i + 1];
+      if (MASKED) {
+        if (chunk_col(c, 2 * i, quad) > lim[e]) a = -INFINITY;
+        if (chunk_col(c, 2 * i + 1, quad) > lim[e]) b = -INFINITY;
+      }
+      mx[e] = fmaxf(mx[e], fmaxf(a, b));
+      const float2 x = ffma2(make_float2(a, b), sl, make_float2(ref[e], ref[e]));
+      float2 t;
+      if (!MASKED && i % EX_FMA_EVERY == EX_FMA_EVERY - 1 - (c & 1))   // masked scores are -inf: their terms are exactly 0
+        t = ex2_fma(x);
+      else
+        t = make_float2(ex2(x.x), ex2(x.y));
+      sm[e] = ffma2(t, make_float2(1.f, 1.f), sm[e]);
+      __nv_bfloat162 hh = __floats2bfloat162_rn(t.x, t.y);
+      pk[8 * c + i] = *reinterpret_cast<uint32_t*>(&hh);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    mx[e] = quad_max(mx[e]);
+    sum[e] = sm[e].x + sm[e].y;
+  }
+}
+__device__ __forceinline__ void ex_terms(uint32_t tS, bool masked, const int (&lim)[2], int quad, const float (&m)[2],
+                                         float sl2, uint32_t (&pk)[32], float (&mx)[2], float (&sum)[2]) {
+  const float ref[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
+  if (masked)
+    ex_terms_t<true>(tS, lim, quad, ref, sl2, pk, mx, sum);
+  else
+    ex_terms_t<false>(tS, lim, quad, ref, sl2, pk, mx, sum);
+  mx[0] *= sl2;
+  mx[1] *= sl2;
+}
+// w[g] of lane l of a quad becomes w[l] of lane g
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int quad) {
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if (g & b) continue;
+      const bool up = quad & b;
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[g] : w[g | b], b);
+      if (up) w[g] = got; else w[g | b] = got;
+    }
+  }
+}
 
 // Instruction descriptor: as idesc_bf16 with B in MN-major order (bit 16)
 constexpr uint32_t EX_IDESC_S = idesc_bf16(128, 128);
@@ -162,6 +326,13 @@ constexpr uint32_t EX_IDESC_PV = idesc_bf16(128, 128) | (1u << 16);
 __device__ __forceinline__ uint64_t v_desc(uint32_t smem_addr) {
   return (uint64_t)((smem_addr >> 4) & 0x3FFF) | ((uint64_t)(ExSmem::SUB >> 4) << 16) |
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(ok));
+  return ok != 0;
 }
 
 // waits a short time for a phase, whatever the error word says
@@ -183,27 +354,30 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   long long* sh_sum = reinterpret_cast<long long*>(smem + S::KV_OFF);   // until the first copies
   const uint32_t q_full = smem_u32(bars), q_empty = smem_u32(bars + 1);
   const uint32_t kv_full0 = smem_u32(bars + 2), kv_empty0 = smem_u32(bars + 2 + EX_SLOTS);
-  const uint32_t land = smem_u32(bars + 2 + 2 * EX_SLOTS), drain = smem_u32(bars + 3 + 2 * EX_SLOTS);
-  const uint32_t tb0 = smem_u32(bars + 4 + 2 * EX_SLOTS);   // per tile: S full, P full, O full
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 10 + 2 * EX_SLOTS);
-#define S_FULL(t) (tb0 + 24 * (t))
-#define P_FULL(t) (tb0 + 24 * (t) + 8)
-#define O_FULL(t) (tb0 + 24 * (t) + 16)
+  const uint32_t land0 = smem_u32(bars + 2 + 2 * EX_SLOTS);   // a V block with rows to be zeroed has landed
+  const uint32_t tb0 = smem_u32(bars + 2 + 3 * EX_SLOTS);     // per tile: S full, P full, O full, drained, turn
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 12 + 3 * EX_SLOTS);
+#define S_FULL(t) (tb0 + 40 * (t))
+#define P_FULL(t) (tb0 + 40 * (t) + 8)
+#define O_FULL(t) (tb0 + 40 * (t) + 16)
+#define DRAINED(t) (tb0 + 40 * (t) + 24)
+#define TURN(t) (tb0 + 40 * (t) + 32)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0 && lane == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);                       // both MMA warps
     for (int i = 0; i < EX_SLOTS; ++i) {
       mbar_init(kv_full0 + 8 * i, 1);
-      mbar_init(kv_empty0 + 8 * i, 1);
+      mbar_init(kv_empty0 + 8 * i, 2);
+      mbar_init(land0 + 8 * i, 1);
     }
-    mbar_init(land, 1);
-    mbar_init(drain, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(S_FULL(t), 1);
-      mbar_init(P_FULL(t), 4);
+      mbar_init(P_FULL(t), 8);
+      mbar_init(TURN(t), 1);
       mbar_init(O_FULL(t), 1);
+      mbar_init(DRAINED(t), 1);
     }
     mbar_fence_init();
     tma_prefetch(&tmQ);
@@ -214,7 +388,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   griddep_wait();
   griddep_launch();
 
-  // the range of this CTA: its first block's sequence, head, unit and block
+  // the range of this CTA: where it starts (sequence, head, unit, step) and its length
   {
     const int per_t = (p.g.S + EX_THREADS - 1) / EX_THREADS;
     const int s0 = threadIdx.x * per_t, s1 = min(p.g.S, s0 + per_t);
@@ -226,7 +400,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
     sh_sum[threadIdx.x] = sum;
     __syncthreads();
-    if (warp == 0) {                             // inclusive scan, twelve sums a lane
+    if (warp == 0) {                             // inclusive scan, twenty sums a lane
       long long mine = 0;
       for (int i = 0; i < EX_THREADS / 32; ++i) mine += sh_sum[lane * (EX_THREADS / 32) + i];
       long long x = mine;
@@ -243,7 +417,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     __syncthreads();
     const long long N = sh_sum[EX_THREADS - 1];
     long long per = (N + gridDim.x - 1) / gridDim.x;
-    if (per < EX_MIN_BLOCKS) per = EX_MIN_BLOCKS;
+    if (per < EX_MIN_COST) per = EX_MIN_COST;
     const long long a = min(N, blockIdx.x * per), b = min(N, a + per);
     const long long mine0 = sh_sum[threadIdx.x] - sum;
     if (b > a && a >= mine0 && a < mine0 + sum) {
@@ -279,23 +453,21 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const uint32_t tbase = *tmem_holder;           // tile t: S and P at 256 t, O at 256 t + 128
   ExWalk w;
   w.left = sh_left;
-  const bool any = w.left > 0;
-  if (any) {
+  if (w.left > 0) {
     w.s = sh_pos[0];
     w.g = sh_pos[1];
     w.u = sh_pos[2];
-    w.kb0 = sh_pos[3];
+    w.at = sh_pos[3];
     w.q.load(p, w.s);
   }
-  const bool mid_start = any && w.kb0 > 0;       // the first item continues a unit
 
-  // registers go from the first four warps to the softmax warps: 128 * (88 + 208 + 208) = 384 * 168
+  // registers go from the first four warps to the softmax warps: 128 * 64 + 512 * 104 = 640 * 96
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0) {
     // ---- producer: lane i loads page i of a block
     const int br = min(p.g.page(), EX_BK);       // rows of a box
-    int kv = 0, items = 0, landed = 0;
+    int kv = 0, items = 0;
     bool ok = true;
     auto load_block = [&](const CUtensorMap* m, int kb, bool is_v) {
       const int slot = kv % EX_SLOTS;
@@ -303,8 +475,8 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       const uint32_t dst = smem_u32(smem + S::KV_OFF + slot * 2 * S::SUB);
       const int valid = max(0, min(EX_BK, w.q.len - kb * EX_BK));
       const int nbox = (valid + br - 1) / br;
-      const bool part = is_v && valid < EX_BK;   // rows behind the last token
-      const uint32_t bar = part ? land : kv_full0 + 8 * slot;
+      // rows behind the last token: the block lands for the V-tail warp first
+      const uint32_t bar = (is_v && valid < EX_BK ? land0 : kv_full0) + 8 * slot;
       if (lane == 0) mbar_arrive_tx(bar, nbox * br * 256);
       __syncwarp();
       if (lane < nbox) {
@@ -313,18 +485,6 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const int row = ((e * p.g.G + w.g) << p.g.shift) + (pos & (p.g.page() - 1));
         tma_load_2d(dst + lane * br * 128, m, bar, 0, row);
         tma_load_2d(dst + S::SUB + lane * br * 128, m, bar, 64, row);
-      }
-      if (part) {
-        if (!mbar_wait_warp(land, landed & 1, p.err)) return false;
-        ++landed;
-        uint8_t* base = smem + S::KV_OFF + slot * 2 * S::SUB;
-        for (int i = lane; i < (EX_BK - valid) * 16; i += 32) {
-          const int row = valid + (i >> 4), c = i & 15;
-          *reinterpret_cast<uint4*>(base + (c >> 3) * S::SUB + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv_full0 + 8 * slot);
       }
       ++kv;
       return true;
@@ -344,214 +504,253 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) ok = load_block(&tmK, kb, false) && load_block(&tmV, kb, true);
     }
     if (!ok) {   // gave up: let the copies in flight land before the CTA ends
-      for (int i = max(0, kv - EX_SLOTS); i < kv; ++i) drain_wait(kv_full0 + 8 * (i % EX_SLOTS), (i / EX_SLOTS) & 1);
+      for (int i = max(0, kv - EX_SLOTS); i < kv; ++i) {
+        drain_wait(kv_full0 + 8 * (i % EX_SLOTS), (i / EX_SLOTS) & 1);
+        drain_wait(land0 + 8 * (i % EX_SLOTS), 0);
+      }
       drain_wait(q_full, items & 1);
-      drain_wait(land, landed & 1);
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      int kv = 0, items = 0, np[2] = {0, 0};
-      bool ok = true;
-      auto kv_base = [&](int i) { return smem_u32(smem + S::KV_OFF + (i % EX_SLOTS) * 2 * S::SUB); };
-      auto wait_kv = [&](int i) { return mbar_wait(kv_full0 + 8 * (i % EX_SLOTS), (i / EX_SLOTS) & 1, p.err); };
-      auto issue_s = [&](int t, int i) {
-        const uint32_t kb = kv_base(i), qb = smem_u32(smem + S::Q_OFF + 2 * t * S::SUB);
+  } else if (warp == 3) {
+    // ---- V tails: zero the rows behind a sequence's last token before the products read them
+    int kv = 0;
+    uint32_t par = 0;                            // bit i: parity of the next landing in slot i
+    bool ok = true;
+    for (bool more = w.open(p); more && ok; more = w.next(p)) {
+      const int nbk = w.kb1 - w.kb0, slot = (kv + 2 * nbk - 1) % EX_SLOTS;
+      const int valid = max(0, w.q.len - (w.kb1 - 1) * EX_BK);   // of the last block; the others are whole
+      kv += 2 * nbk;
+      if (valid >= EX_BK) continue;
+      ok = mbar_wait_warp(land0 + 8 * slot, (par >> slot) & 1, p.err);
+      if (!ok) break;
+      par ^= 1u << slot;
+      uint8_t* base = smem + S::KV_OFF + slot * 2 * S::SUB;
+      for (int i = lane; i < (EX_BK - valid) * 16; i += 32) {
+        const int row = valid + (i >> 4), c = i & 15;
+        *reinterpret_cast<uint4*>(base + (c >> 3) * S::SUB + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kv_full0 + 8 * slot);
+    }
+  } else {
+    // ---- MMA warp of tile t: the whole warp walks in step, one elected lane issues.  A product is
+    // accepted only as the last one runs (64 cycles each), so whatever a warp does between its
+    // products would leave the tensor core idle; with a warp per tile the other one's products run then.
+    const int t = warp - 1;
+    const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0) + 256 * t;
+    const uint64_t qd = sw128_desc(smem_u32(smem + S::Q_OFF) + t * (2 * S::SUB));
+    int kv = 0, items = 0, np = 0, turns = 0;
+    bool ok = true;
+    auto kv_base = [&](int i) { return smem_u32(smem + S::KV_OFF) + (uint32_t)(i % EX_SLOTS) * (2 * S::SUB); };
+    auto wait_kv = [&](int i) { return mbar_wait_warp(kv_full0 + 8 * (i % EX_SLOTS), (i / EX_SLOTS) & 1, p.err); };
+    // S = Q K^T of fill i, and what else is done once the products issued so far are
+    auto issue_s = [&](int i, bool last) {
+      if (elect_one()) {
+        const uint64_t kd = sw128_desc(kv_base(i));
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_bf16(tbase + 256 * t, sw128_desc(qb + (kk >> 2) * S::SUB) + 2 * (kk & 3),
-                    sw128_desc(kb + (kk >> 2) * S::SUB) + 2 * (kk & 3), EX_IDESC_S, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk) {         // 16 head dims a step
+          const uint64_t off = (kk >> 2) * (S::SUB >> 4) + 2 * (kk & 3);
+          umma_bf16(tb, qd + off, kd + off, EX_IDESC_S, kk > 0 ? 1u : 0u);
+        }
         umma_commit(S_FULL(t));
-      };
-      auto issue_pv = [&](int t, int i, bool first) {
+        umma_commit(kv_empty0 + 8 * (i % EX_SLOTS));
+        if (last) umma_commit(q_empty);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int i, bool first, bool last) {
+      if (elect_one()) {
         const uint64_t vd = v_desc(kv_base(i));
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)   // 16 keys a step: 2048 bytes of V, 8 columns of P
-          umma_bf16_ta(tbase + 256 * t + 128, tbase + 256 * t + 8 * kk, vd + 128 * kk, EX_IDESC_PV,
-                       (!first || kk > 0) ? 1u : 0u);
-      };
-      for (bool more = w.open(p); more && ok; more = w.next(p), ++items) {
-        const int nt = w.tokens_of(p, 1) > 0 ? 2 : 1, nbk = w.kb1 - w.kb0;
-        ok = mbar_wait(q_full, items & 1, p.err) && wait_kv(kv);
+        for (int kk = 0; kk < 8; ++kk)           // 16 keys a step: 2048 bytes of V, 8 columns of P
+          umma_bf16_ta(tb + 128, tb + 8 * kk, vd + 128 * kk, EX_IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+        umma_commit(kv_empty0 + 8 * (i % EX_SLOTS));
+        if (last) umma_commit(O_FULL(t));
+      }
+      __syncwarp();
+    };
+    for (bool more = w.open(p); __any_sync(0xffffffffu, more) && ok; more = w.next(p), ++items) {
+      const bool both = __any_sync(0xffffffffu, w.tokens_of(p, 1) > 0), has = both || t == 0;
+      const int nbk = __shfl_sync(0xffffffffu, w.kb1 - w.kb0, 0);
+      ok = mbar_wait_warp(q_full, items & 1, p.err);
+      if (!ok) break;
+      if (!has) {                                // no tile B: its share of the releases
+        if (lane == 0) mbar_arrive(q_empty);
+        for (int j = 0; j < 2 * nbk && ok; ++j) {
+          ok = wait_kv(kv + j);                  // this fill's, not an earlier one's
+          if (ok && lane == 0) mbar_arrive(kv_empty0 + 8 * ((kv + j) % EX_SLOTS));
+        }
+      } else {
+        ok = wait_kv(kv);
         if (!ok) break;
         tc_fence_after();
-        for (int t = 0; t < nt; ++t) issue_s(t, kv);
-        umma_commit(kv_empty0 + 8 * (kv % EX_SLOTS));
-        if (nbk == 1) umma_commit(q_empty);
-        for (int j = 0; j < nbk && ok; ++j) {
-          const int vi = kv + 2 * j + 1, ki = kv + 2 * j + 2;
+        issue_s(kv, nbk == 1);
+        for (int j = 0; j < nbk; ++j) {
+          const int vi = kv + 2 * j + 1;
           const bool last = j + 1 == nbk;
-          ok = wait_kv(vi);
-          for (int t = 0; t < nt && ok; ++t) {
-            ok = mbar_wait(P_FULL(t), np[t] & 1, p.err);
+          ok = wait_kv(vi) && (last || wait_kv(vi + 1)) && mbar_wait_warp(P_FULL(t), np & 1, p.err);
+          if (!ok) break;
+          ++np;
+          // the tiles take turns, PV and the next S together: mixed, both would end late and both softmaxes run at once
+          if (both) {
+            ok = mbar_wait_warp(TURN(t), (turns & 1) ^ (t == 0), p.err);
             if (!ok) break;
-            ++np[t];
-            tc_fence_after();
-            issue_pv(t, vi, j == 0);
-            if (t == nt - 1) umma_commit(kv_empty0 + 8 * (vi % EX_SLOTS));
-            if (last) {
-              umma_commit(O_FULL(t));
-            } else {
-              if (t == 0) {
-                ok = wait_kv(ki);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              issue_s(t, ki);
-              if (t == nt - 1) {
-                umma_commit(kv_empty0 + 8 * (ki % EX_SLOTS));
-                if (j + 2 == nbk) umma_commit(q_empty);
-              }
-            }
+            ++turns;
           }
+          tc_fence_after();
+          issue_pv(vi, j == 0, last);
+          if (!last) issue_s(vi + 1, j + 2 == nbk);
+          if (both && lane == 0) mbar_arrive(TURN(t ^ 1));
         }
-        kv += 2 * nbk;
       }
-      umma_commit(drain);
-      drain_wait(drain, 0);
+      kv += 2 * nbk;
     }
+    if (elect_one()) umma_commit(DRAINED(t));
+    __syncwarp();
+    drain_wait(DRAINED(t), 0);
+    __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    // ---- softmax of tile t: thread = row
-    const int t = (warp - 4) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tS = tbase + 256 * t + lane_off, tO = tS + 128;
-    const int tok_r = r / p.rep, head_r = r % p.rep;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ---- softmax of tile t: 16 rows a warp, two rows a quad of lanes
+    const int t = (warp - 4) >> 3, quad = lane & 3;
+    const int row0 = (warp & 3) * 32 + ((warp >> 2) & 1) * 16;   // of the warp; warps reach the lanes of their quarter
+    const uint32_t tS = tbase + 256 * t + ((uint32_t)row0 << 16), tO = tS + 128;
+    const int r[2] = {row0 + (lane >> 2), row0 + (lane >> 2) + 8};
+    const int tok_r[2] = {r[0] / p.rep, r[1] / p.rep};
     int ns = 0, no = 0;
     bool ok = true, first_item = true;
+    const bool scribe = t == 0 && row0 == 0 && lane == 0;
+    if (scribe) p.meta[blockIdx.x].tail = p.meta[blockIdx.x].head = 0;
     for (bool more = w.open(p); more && ok; more = w.next(p), first_item = false) {
       const int nt = w.tokens_of(p, t);
       const bool whole = w.kb0 == 0 && w.kb1 == w.nb;
-      if (r == 0 && t == 0) {
+      if (scribe) {
         ExMeta* m = p.meta + blockIdx.x;
         if (first_item) {
-          m->head = mid_start;
+          m->head = w.kb0 > 0;
           m->ends = w.kb1 == w.nb;
         }
-        const bool tail = w.kb0 == 0 && w.kb1 < w.nb;   // only the last item can be one
-        m->tail = tail;
+        m->tail = w.kb0 == 0 && w.kb1 < w.nb;    // only the last item can be one
         m->s = w.s;
         m->g = w.g;
         m->u = w.u;
       }
       if (nt == 0) continue;                     // the unit has no tile B
-      const int tok = (2 * w.u + t) * p.tpt + tok_r;   // of the sequence's new tokens
-      const bool row_in = tok_r < nt;
-      const int pos = row_in ? w.q.len - w.q.n + tok : -1;
-      float m = -INFINITY, l = 0.f;
+      const int tok0 = (2 * w.u + t) * p.tpt;    // of the sequence's new tokens
+      const bool row_in[2] = {tok_r[0] < nt, tok_r[1] < nt};
+      const int pos[2] = {row_in[0] ? w.q.len - w.q.n + tok0 + tok_r[0] : -1,
+                          row_in[1] ? w.q.len - w.q.n + tok0 + tok_r[1] : -1};
+      // pend: factor that O still has to be scaled by
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, pend[2] = {1.f, 1.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++ns) {
         ok = mbar_wait_warp(S_FULL(t), ns & 1, p.err);
         if (!ok) break;
         tc_fence_after();
-        float s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s + 32 * c);
-        tmem_wait_ld();
-        const int lim = pos - kb * EX_BK;        // keys c <= lim are seen
-        if (!__all_sync(0xffffffffu, lim >= EX_BK - 1)) {
-#pragma unroll
-          for (int c = 0; c < EX_BK; ++c)
-            if (c > lim) s[c] = -INFINITY;
+        const int lim[2] = {pos[0] - kb * EX_BK, pos[1] - kb * EX_BK};   // keys c <= lim are seen
+        const bool masked = !__all_sync(0xffffffffu, lim[0] >= EX_BK - 1 && lim[1] >= EX_BK - 1);
+        // The terms are formed against the reference from the blocks before, while this block's
+        // maximum is found on the way; P replaces S only afterwards.  A reference up to 2^EX_REDO
+        // too low does no harm (P and O have fp32's exponents): it is raised for the next block.
+        // Where it is lower still the warp forms the block again.
+        uint32_t pk[32];
+        float mx[2], sum[2];
+        if (kb == w.kb0) {
+          ex_row_max(tS, masked, lim, quad, mx);
+          m[0] = mx[0] * p.sl2;
+          m[1] = mx[1] * p.sl2;
         }
-        float mx4[4] = {s[0], s[1], s[2], s[3]};
+        ex_terms(tS, masked, lim, quad, m, p.sl2, pk, mx, sum);
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + EX_REDO || mx[1] > m[1] + EX_REDO)) {
 #pragma unroll
-        for (int c = 4; c < 124; c += 8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx4[i] = max3(mx4[i], s[c + i], s[c + 4 + i]);
+          for (int e = 0; e < 2; ++e) {
+            if (mx[e] > m[e] + EX_REDO) {
+              const float corr = ex2(m[e] - mx[e]);
+              l[e] *= corr;
+              pend[e] *= corr;
+              m[e] = mx[e];
+            }
+          }
+          ex_terms(tS, masked, lim, quad, m, p.sl2, pk, mx, sum);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], s[124 + i]);
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.sl2;
-        float corr = 1.f;
-        if (mx > m + 8.f) {                      // also the first finite maximum (m = -inf)
-          corr = ex2(m - mx);
-          m = mx;
-        }
-        // the products that read O's last value are done: S_j was issued after them
-        if (kb > w.kb0 && __any_sync(0xffffffffu, corr != 1.f)) {
+        // the product that wrote O last is done: S_j was issued after it
+        if (kb > w.kb0 && __any_sync(0xffffffffu, pend[0] != 1.f || pend[1] != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tmem_ld32(tO + 32 * c, o);
-            tmem_wait_ld();
+            float o[16];
+            tmem_ld_16x256b(tO + 32 * c, o);
+            tmem_wait_ld16(o);
 #pragma unroll
-            for (int k2 = 0; k2 < 32; ++k2) o[k2] *= corr;
-            tmem_st32(tO + 32 * c, o);
+            for (int k = 0; k < 16; ++k) o[k] *= pend[(k >> 1) & 1];
+            tmem_st_16x256b(tO + 32 * c, o);
           }
-          tmem_wait_st();
         }
-        const float ref = m == -INFINITY ? 0.f : -m;
-        const float2 sl = make_float2(p.sl2, p.sl2), rf = make_float2(ref, ref);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 x = ffma2(make_float2(s[64 * hf + 2 * i], s[64 * hf + 2 * i + 1]), sl, rf);
-            const float ea = ex2(x.x), eb = ex2(x.y);
-            sum[i & 3] += ea + eb;
-            __nv_bfloat162 hh = __floats2bfloat162_rn(ea, eb);
-            pk[i] = *reinterpret_cast<uint32_t*>(&hh);
-          }
-          tmem_st32u(tS + 32 * hf, pk);
-        }
-        l = l * corr + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        tmem_st_16x128b(tS, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(P_FULL(t));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[e] += sum[e];
+          pend[e] = 1.f;
+          if (mx[e] > m[e] + EX_RAISE) {
+            pend[e] = ex2(m[e] - mx[e]);
+            l[e] *= pend[e];
+            m[e] = mx[e];
+          }
+        }
       }
       if (!ok) break;
+      l[0] = quad_sum(l[0]);
+      l[1] = quad_sum(l[1]);
       ok = mbar_wait_warp(O_FULL(t), no & 1, p.err);
       ++no;
       if (!ok) break;
       tc_fence_after();
-      if (whole) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const long long row = w.q.q0 + tok;
-        const int head = w.g * p.rep + head_r;
-        bf16* dst = p.o + row * p.ld_o + (long long)head * PG_D;
-        if (row_in && p.lse)
-          p.lse[row * p.H + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-          if (row_in) {
+      const long long part = ((long long)(2 * blockIdx.x + (w.kb0 == 0)) * 2 + t) * 128;   // continued: 0, begun here: 1
+      float f[2];
+      bf16* dst[2];
+      float* pdst[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint4 u;
-              __nv_bfloat162* hh = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) hh[i] = __floats2bfloat162_rn(o[8 * k + 2 * i] * inv, o[8 * k + 2 * i + 1] * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) = u;
-            }
-          }
+      for (int e = 0; e < 2; ++e) {
+        const long long row = w.q.q0 + tok0 + tok_r[e];
+        const int head = w.g * p.rep + r[e] % p.rep;
+        f[e] = whole ? (l[e] > 0.f ? pend[e] / l[e] : 0.f) : pend[e];
+        dst[e] = p.o + row * p.ld_o + (long long)head * PG_D;
+        pdst[e] = p.part_o + (part + r[e]) * PG_D;
+        if (row_in[e] && quad == 0) {
+          if (!whole)
+            *reinterpret_cast<float2*>(p.part_ml + (part + r[e]) * 2) = make_float2(m[e], l[e]);
+          else if (p.lse)
+            p.lse[row * p.H + head] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.6931471805599453f : -INFINITY;
         }
-      } else {
-        const int slot = 2 * blockIdx.x + (w.kb0 == 0);   // continued: 0, begun here: 1
-        float* dst = p.part_o + ((long long)slot * 256 + t * 128 + r) * PG_D;
-        if (row_in) *reinterpret_cast<float2*>(p.part_ml + ((long long)slot * 256 + t * 128 + r) * 2) = make_float2(m, l);
+      }
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float o[32];
-          tmem_ld32(tO + 32 * c, o);
-          tmem_wait_ld();
-          if (row_in) {
+      for (int c = 0; c < 4; ++c) {
+        float o[16];
+        tmem_ld_16x256b(tO + 32 * c, o);
+        tmem_wait_ld16(o);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(dst + 32 * c + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        for (int e = 0; e < 2; ++e) {
+          if (whole) {                           // eight columns a lane after the transpose
+            uint32_t x[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              __nv_bfloat162 hh = __floats2bfloat162_rn(o[4 * g + 2 * e] * f[e], o[4 * g + 2 * e + 1] * f[e]);
+              x[g] = *reinterpret_cast<uint32_t*>(&hh);
+            }
+            quad_transpose(x, quad);
+            if (row_in[e]) *reinterpret_cast<uint4*>(dst[e] + 32 * c + 8 * quad) = make_uint4(x[0], x[1], x[2], x[3]);
+          } else if (row_in[e]) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<float2*>(pdst[e] + 32 * c + 8 * g + 2 * quad) =
+                  make_float2(o[4 * g + 2 * e] * f[e], o[4 * g + 2 * e + 1] * f[e]);
           }
         }
       }
       tc_fence_before();   // O is read before the next item's first product is issued (after its P)
-    }
-    if (!any && r == 0 && t == 0) {
-      p.meta[blockIdx.x].tail = 0;
-      p.meta[blockIdx.x].head = 0;
     }
   }
   tc_fence_before();
@@ -564,6 +763,8 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #undef S_FULL
 #undef P_FULL
 #undef O_FULL
+#undef DRAINED
+#undef TURN
 
 // CTA (c, y): rows 32 y .. of the unit whose parts begin in CTA c of the kernel above, a warp per
 // row: o = sum of o_i 2^(m_i - m) / sum of l_i 2^(m_i - m), in the order of the parts.
