@@ -26,6 +26,8 @@
 // (log2 units), then O is rescaled in tensor memory; terms stay below 2^8.  Rows of V behind
 // the sequence's last token are zeroed in shared memory, their memory may hold anything.
 // Every wait is bounded (see common.cuh).
+#include <climits>
+
 #include "host.hpp"
 #include "pages.cuh"
 
@@ -195,6 +197,11 @@ __device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
                :
                : "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
@@ -224,7 +231,7 @@ __device__ __forceinline__ void ex_row_max(uint32_t tS, bool masked, const int (
   mx[1] = quad_max(mx[1]);
 }
 
-constexpr int EX_FMA_EVERY = 4;    // of the pairs of terms, one in so many goes to ex2_fma
+constexpr int EX_FMA_EVERY = 8;    // of the pairs of terms, one in so many goes to ex2_fma
 constexpr float EXC0 = 0.99999926144f, EXC1 = 0.69312181475f, EXC2 = 0.24024744849f, EXC3 = 0.05591786025f,
                 EXC4 = 0.00957010107f;
 
@@ -274,7 +281,7 @@ __device__ __forceinline__ void ex_terms_t(uint32_t tS, const int (&lim)[2], int
         if (chunk_col(c, 2 * i, quad) > lim[e]) a = -INFINITY;
         if (chunk_col(c, 2 * i + 1, quad) > lim[e]) b = -INFINITY;
       }
-      mx[e] = fmaxf(mx[e], fmaxf(a, b));
+      mx[e] = max3(mx[e], a, b);
       const float2 x = ffma2(make_float2(a, b), sl, make_float2(ref[e], ref[e]));
       float2 t;
       if (!MASKED && i % EX_FMA_EVERY == EX_FMA_EVERY - 1 - (c & 1))   // masked scores are -inf: their terms are exactly 0
@@ -639,8 +646,9 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       if (nt == 0) continue;                     // the unit has no tile B
       const int tok0 = (2 * w.u + t) * p.tpt;    // of the sequence's new tokens
       const bool row_in[2] = {tok_r[0] < nt, tok_r[1] < nt};
-      const int pos[2] = {row_in[0] ? w.q.len - w.q.n + tok0 + tok_r[0] : -1,
-                          row_in[1] ? w.q.len - w.q.n + tok0 + tok_r[1] : -1};
+      // rows without a token hold anything and are never written: let them see everything, masks cost time
+      const int pos[2] = {row_in[0] ? w.q.len - w.q.n + tok0 + tok_r[0] : INT_MAX,
+                          row_in[1] ? w.q.len - w.q.n + tok0 + tok_r[1] : INT_MAX};
       // pend: factor that O still has to be scaled by
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, pend[2] = {1.f, 1.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++ns) {

@@ -461,33 +461,38 @@ class Attention:
     def _paged(self, x, cache, layer, tokens, q_start, residual, out, stream):
         if self.shape.n_kv_heads != cache.data.shape[2]:
             raise ValueError("the cache holds %d KV heads" % cache.data.shape[2])
-        named = [("x", x), ("w_o", self.w_o)] + [(n, t) for n, t in (("residual", residual), ("out", out),
-                                                                   ("q_start", q_start)) if t is not None]
-        paged._same_device(cache.data, named)
+        named = (("x", x), ("w_o", self.w_o)) + tuple(
+            (n, t) for n, t in (("residual", residual), ("out", out), ("q_start", q_start)) if t is not None)
+        index = paged._same_device(cache.data, named)
         for t, name in ((x, "x"), (residual, "residual"), (out, "out")):
             _contig(t, name)
             if t is not None and (tuple(t.shape) != (tokens, self.shape.d_model) or t.dtype != self.w_o.dtype):
                 raise ValueError("%s must be %s [%d, %d]" % (name, self.w_o.dtype, tokens, self.shape.d_model))
-        cfg, k, v = cache.config(layer)
-        n = ctypes.c_size_t()
-        L, a, p = lib(), ctypes.byref(self.cfg), ctypes.byref(cfg)
-        with paged._Call(cache.data.device, stream) as st:
+        sizes, k, v = cache.config(layer)
+        cfg = sizes.ref
+        a = ctypes.byref(self.cfg)
+        w = ctypes.byref(self.w)
+
+        def body(st, out):
+            L = lib()
             out = torch.empty_like(x) if out is None else out
             if tokens == 0:
                 return out
+            n = ctypes.c_size_t()
             if q_start is None:
-                check(L.jamba_attn_paged_step_workspace_size(a, p, ctypes.byref(n)))
+                check(L.jamba_attn_paged_step_workspace_size(a, cfg, ctypes.byref(n)))
             else:
-                check(L.jamba_attn_paged_prefill_workspace_size(a, p, tokens, ctypes.byref(n)))
+                check(L.jamba_attn_paged_prefill_workspace_size(a, cfg, tokens, ctypes.byref(n)))
             ws = torch.empty(n.value, dtype=torch.uint8, device=x.device)
             if q_start is None:
-                check(L.jamba_attn_paged_step(a, ctypes.byref(self.w), p, _p(x), _p(residual), _p(out), _p(k), _p(v),
-                                              _p(cache.table), _p(cache.lengths), _p(ws), ws.numel(), st))
+                check(L.jamba_attn_paged_step(a, w, cfg, _p(x), _p(residual), _p(out), _p(k), _p(v), _p(cache.table),
+                                              _p(cache.lengths), _p(ws), ws.numel(), st))
             else:
-                check(L.jamba_attn_paged_prefill(a, ctypes.byref(self.w), p, _p(x), _p(residual), _p(out), tokens,
-                                                 _p(q_start), _p(k), _p(v), _p(cache.table), _p(cache.lengths),
-                                                 _p(ws), ws.numel(), st))
-        return out
+                check(L.jamba_attn_paged_prefill(a, w, cfg, _p(x), _p(residual), _p(out), tokens, _p(q_start), _p(k),
+                                                 _p(v), _p(cache.table), _p(cache.lengths), _p(ws), ws.numel(), st))
+            return out
+
+        return paged._run(index, stream, body, out)
 
     def paged_prefill(self, x, q_start, cache, layer=0, residual=None, out=None, stream=None):
         """x [tokens, d_model], the new tokens of all slots of a PagedKVCache one

@@ -10,6 +10,7 @@ that device's current stream); outputs and workspaces are allocated on that
 stream, per call, so calls on several streams and captured graphs share none.
 """
 import ctypes
+import functools
 
 import torch
 
@@ -17,194 +18,243 @@ from . import _abi
 from ._abi import check, lib
 
 HEAD_DIM = 128
+_BF16 = torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-class _Call:
-    """The device and stream of one call: entered, both are current, so that
-    allocations and launches go there."""
+class _On:
+    """Makes a device and a stream current, so that allocations and launches go there."""
 
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
+    def __init__(self, index, stream):
+        self.index, self.stream = index, stream
 
     def __enter__(self):
-        self.guards = []
-        if torch.cuda.current_device() != self.device.index:
-            self.guards.append(torch.cuda.device(self.device))
+        self.guards = [torch.cuda.device(self.index)]
         if self.stream is not None:
             self.guards.append(torch.cuda.stream(self.stream))
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
 
+def _run(index, stream, body, *args):
+    """body(raw stream, *args) on device `index` and `stream` (None: the device's current one)."""
+    if stream is None and torch.cuda.current_device() == index:
+        return body(_raw_stream(index), *args)
+    with _On(index, stream) as raw:
+        return body(raw, *args)
+
+
 def _same_device(first, named):
-    if not first.is_cuda:
-        raise ValueError("libjamba works on CUDA tensors only")
+    """The index of the CUDA device that all are on."""
+    index = first.get_device()
     for name, t in named:
-        if not t.is_cuda:
-            raise ValueError("libjamba works on CUDA tensors only")
-        if t.device != first.device:
+        if t.get_device() != index:
+            if index < 0 or not t.is_cuda:
+                raise ValueError("libjamba works on CUDA tensors only")
             raise ValueError("%s is on %s, the pages on %s" % (name, t.device, first.device))
+    if index < 0:
+        raise ValueError("libjamba works on CUDA tensors only")
+    return index
 
 
 def _ints(t, name, shape):
     if t.dtype != torch.int32:
         raise ValueError("%s must be int32" % name)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must have shape %s" % (name, list(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
 
 
+class _Sizes:
+    """A jamba_pages_config, by reference, and the workspace bytes asked for with it."""
+
+    def __init__(self, *fields):
+        self.ref = ctypes.byref(_abi.PagesConfig(*fields))
+        self.known = {}
+
+    def workspace(self, index, size_of, *args):
+        """What entry point `size_of` says for these sizes on the current device, number `index`."""
+        key = (index, size_of) + args
+        found = self.known.get(key)
+        if found is None:
+            if len(self.known) >= 256:
+                self.known.clear()
+            n = ctypes.c_size_t()
+            check(getattr(lib(), size_of)(self.ref, *args, ctypes.byref(n)))
+            found = self.known[key] = max(n.value, 16)
+        return found
+
+
+_sizes = functools.lru_cache(maxsize=1024)(_Sizes)
+
+
 def _config(num_pages, n_kv_heads, page_size, planes, table, lengths):
-    if table.dim() != 2 or table.dtype != torch.int32 or (table.numel() and table.stride(1) != 1):
+    if table.dim() != 2 or table.dtype != torch.int32:
         raise ValueError("table must be int32 [max_seqs, max_pages] with unit-stride rows")
     S, W = table.shape
+    ld, one = table.stride()
+    if one != 1 and W > 1:
+        raise ValueError("table must be int32 [max_seqs, max_pages] with unit-stride rows")
     _ints(lengths, "lengths", (S,))
-    return _abi.PagesConfig(num_pages, page_size, n_kv_heads, HEAD_DIM, planes, S, W,
-                            table.stride(0) if S > 1 else W, _abi.JAMBA_BF16)
+    return _sizes(num_pages, page_size, n_kv_heads, HEAD_DIM, planes, S, W, ld if S > 1 else W, _abi.JAMBA_BF16)
 
 
 def _planes(k_pages, v_pages):
+    """Their shape [num_pages, n_kv_heads, page_size, 128]."""
+    shape = k_pages.shape
     for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t.dim() != 4 or t.shape[3] != HEAD_DIM or t.dtype != torch.bfloat16 or not t.is_contiguous():
+        if t.dtype != _BF16 or len(shape) != 4 or shape[3] != HEAD_DIM or not t.is_contiguous():
             raise ValueError("%s must be contiguous bf16 [num_pages, n_kv_heads, page_size, 128]" % name)
-    if k_pages.shape != v_pages.shape:
+    if v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must have one shape")
+    return shape
 
 
 def _rows(t, name, heads=None):
-    """The token stride of t [tokens, heads, 128], its heads next to one another."""
-    if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.dtype != torch.bfloat16 or (heads and t.shape[1] != heads):
+    """(tokens, heads, token stride) of t [tokens, heads, 128], its heads next to one another."""
+    shape = t.shape
+    if t.dtype != _BF16 or len(shape) != 3 or shape[2] != HEAD_DIM or (heads and shape[1] != heads):
         raise ValueError("%s must be bf16 [tokens, %s, 128]" % (name, heads or "heads"))
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM)):
+    T, H, _ = shape
+    ld, head, one = t.stride()
+    if T and H and (one != 1 or (H > 1 and head != HEAD_DIM)):
         raise ValueError("%s must have its heads next to one another" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+    return T, H, ld if T > 1 else H * HEAD_DIM
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _pool(data, refs, table, lengths):
-    if data.dim() != 5 or data.shape[4] != HEAD_DIM or data.dtype != torch.bfloat16 or not data.is_contiguous():
+def _pool(data, refs, table, lengths, *named):
+    shape = data.shape
+    if data.dtype != _BF16 or len(shape) != 5 or shape[4] != HEAD_DIM or not data.is_contiguous():
         raise ValueError("data must be contiguous bf16 [planes, num_pages, n_kv_heads, page_size, 128]")
-    _same_device(data, (("refs", refs), ("table", table), ("lengths", lengths)))
-    planes, N, G, P, _ = data.shape
+    index = _same_device(data, (("refs", refs), ("table", table), ("lengths", lengths)) + named)
+    planes, N, G, P, _ = shape
     _ints(refs, "refs", (N,))
-    return _config(N, G, P, planes, table, lengths)
+    return index, _config(N, G, P, planes, table, lengths)
 
 
 def _upkeep_workspace(cfg, device):
-    n = ctypes.c_size_t()
-    check(lib().jamba_pages_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device=device)
+    return torch.empty(cfg.workspace(device.index, "jamba_pages_workspace_size"), dtype=torch.uint8, device=device)
 
 
 def pages_fork(parent, refs, table, lengths, page_size, stream=None):
     """Slot s becomes a fork of slot parent[s] (sharing its pages), stays with
     parent[s] = s, or is freed with parent[s] = -1; all at once, in place."""
-    _same_device(table, (("parent", parent), ("refs", refs), ("lengths", lengths)))
+    index = _same_device(table, (("parent", parent), ("refs", refs), ("lengths", lengths)))
     if refs.dim() != 1:
         raise ValueError("refs must have shape [num_pages]")
-    _ints(refs, "refs", (refs.shape[0],))
+    _ints(refs, "refs", refs.shape)
     cfg = _config(refs.shape[0], 1, page_size, 1, table, lengths)
-    _ints(parent, "parent", (table.shape[0],))
-    with _Call(table.device, stream) as st:
+    _ints(parent, "parent", lengths.shape)
+
+    def body(st):
         ws = _upkeep_workspace(cfg, table.device)
-        check(lib().jamba_pages_fork(ctypes.byref(cfg), _p(parent), _p(refs), _p(table), _p(lengths), _p(ws),
-                                     ws.numel(), st))
+        check(lib().jamba_pages_fork(cfg.ref, _p(parent), _p(refs), _p(table), _p(lengths), _p(ws), ws.numel(), st))
+
+    _run(index, stream, body)
 
 
 def pages_grow(add, data, refs, table, lengths, stream=None):
     """Room for add[s] more tokens in every slot, counted into lengths; a shared
     last page is copied first.  Returns granted [max_seqs] int32 (0: refused,
     the slot is as it was)."""
-    cfg = _pool(data, refs, table, lengths)
-    _same_device(data, (("add", add),))
-    _ints(add, "add", (table.shape[0],))
-    with _Call(data.device, stream) as st:
+    index, cfg = _pool(data, refs, table, lengths, ("add", add))
+    _ints(add, "add", lengths.shape)
+
+    def body(st):
         ws = _upkeep_workspace(cfg, data.device)
-        granted = torch.empty(table.shape[0], dtype=torch.int32, device=data.device)
-        check(lib().jamba_pages_grow(ctypes.byref(cfg), _p(add), _p(data), _p(refs), _p(table), _p(lengths),
-                                     _p(granted), _p(ws), ws.numel(), st))
-    return granted
+        granted = torch.empty_like(lengths)
+        check(lib().jamba_pages_grow(cfg.ref, _p(add), _p(data), _p(refs), _p(table), _p(lengths), _p(granted), _p(ws),
+                                     ws.numel(), st))
+        return granted
+
+    return _run(index, stream, body)
 
 
 def pages_compact(data, refs, table, lengths, stream=None):
     """Moves the live pages to the front of the pool.  Returns remap [num_pages]
     int32: each live page's new number, -1 for free pages."""
-    cfg = _pool(data, refs, table, lengths)
-    with _Call(data.device, stream) as st:
+    index, cfg = _pool(data, refs, table, lengths)
+
+    def body(st):
         ws = _upkeep_workspace(cfg, data.device)
-        remap = torch.empty(data.shape[1], dtype=torch.int32, device=data.device)
-        check(lib().jamba_pages_compact(ctypes.byref(cfg), _p(data), _p(refs), _p(table), _p(lengths), _p(remap),
-                                        _p(ws), ws.numel(), st))
-    return remap
+        remap = torch.empty_like(refs)
+        check(lib().jamba_pages_compact(cfg.ref, _p(data), _p(refs), _p(table), _p(lengths), _p(remap), _p(ws), ws.numel(),
+                                        st))
+        return remap
+
+    return _run(index, stream, body)
 
 
 def paged_append(k, v, k_pages, v_pages, table, lengths, q_start=None, stream=None):
     """Keys and values k, v [tokens, n_kv_heads, 128] of the sequences' last
     tokens into their pages: sequence s has rows q_start[s] .. q_start[s+1] - 1
     (q_start [max_seqs + 1] int32), or one row each without q_start."""
-    _planes(k_pages, v_pages)
-    named = [("k", k), ("v", v), ("v_pages", v_pages), ("table", table), ("lengths", lengths)]
-    _same_device(k_pages, named + ([("q_start", q_start)] if q_start is not None else []))
-    N, G, P, _ = k_pages.shape
+    named = (("k", k), ("v", v), ("v_pages", v_pages), ("table", table), ("lengths", lengths))
+    index = _same_device(k_pages, named if q_start is None else named + (("q_start", q_start),))
+    N, G, P, _ = _planes(k_pages, v_pages)
     cfg = _config(N, G, P, 1, table, lengths)
-    ld = _rows(k, "k", G)
-    if _rows(v, "v", G) != ld or v.shape != k.shape:
+    T, _, ld = _rows(k, "k", G)
+    if _rows(v, "v", G) != (T, G, ld):
         raise ValueError("k and v must have one shape and one token stride")
     if q_start is not None:
         _ints(q_start, "q_start", (table.shape[0] + 1,))
-    if k.shape[0] == 0 and q_start is not None:
-        return
-    with _Call(k_pages.device, stream) as st:
-        check(lib().jamba_paged_append(ctypes.byref(cfg), _p(k), _p(v), ld, k.shape[0], _p(q_start), _p(k_pages),
-                                       _p(v_pages), _p(table), _p(lengths), st))
+        if T == 0:
+            return
+
+    def body(st):
+        check(lib().jamba_paged_append(cfg.ref, _p(k), _p(v), ld, T, _p(q_start), _p(k_pages), _p(v_pages), _p(table),
+                                       _p(lengths), st))
+
+    _run(index, stream, body)
 
 
 def _attend(q, k_pages, v_pages, table, lengths, q_start, out, want_lse, stream):
-    _planes(k_pages, v_pages)
-    named = [("q", q), ("v_pages", v_pages), ("table", table), ("lengths", lengths)]
-    named += [(n, t) for n, t in (("q_start", q_start), ("out", out)) if t is not None]
-    _same_device(k_pages, named)
-    N, G, P, _ = k_pages.shape
-    cfg = _config(N, G, P, 1, table, lengths)
-    S = table.shape[0]
-    ld = _rows(q, "q")
-    T, H, _ = q.shape
+    named = (("q", q), ("v_pages", v_pages), ("table", table), ("lengths", lengths))
     if q_start is not None:
-        _ints(q_start, "q_start", (S + 1,))
-    elif T != S:
-        raise ValueError("q must hold one token for each of the %d slots" % S)
-    L = lib()
-    n = ctypes.c_size_t()
-    with _Call(k_pages.device, stream) as st:
+        named += (("q_start", q_start),)
+    if out is not None:
+        named += (("out", out),)
+    index = _same_device(k_pages, named)
+    N, G, P, _ = _planes(k_pages, v_pages)
+    cfg = _config(N, G, P, 1, table, lengths)
+    T, H, ld = _rows(q, "q")
+    if q_start is not None:
+        _ints(q_start, "q_start", (table.shape[0] + 1,))
+    elif T != table.shape[0]:
+        raise ValueError("q must hold one token for each of the %d slots" % table.shape[0])
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+
+    def body(st, out):
+        L, device = lib(), q.device
         if out is None:
-            out = torch.empty(T, H, HEAD_DIM, dtype=q.dtype, device=q.device)
-        elif out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-        ld_o = _rows(out, "out")
-        lse = torch.empty(T, H, dtype=torch.float32, device=q.device) if want_lse else None
+            out = torch.empty((T, H, HEAD_DIM), dtype=_BF16, device=device)
+        ld_o = _rows(out, "out")[2]
+        lse = torch.empty((T, H), dtype=torch.float32, device=device) if want_lse else None
         if T:
             if q_start is None:
-                check(L.jamba_paged_decode_workspace_size(ctypes.byref(cfg), H, ctypes.byref(n)))
+                ws = torch.empty(cfg.workspace(index, "jamba_paged_decode_workspace_size", H), dtype=torch.uint8,
+                                 device=device)
+                check(L.jamba_paged_decode(cfg.ref, H, _p(q), ld, _p(k_pages), _p(v_pages), _p(table), _p(lengths), _p(out),
+                                           ld_o, _p(lse), _p(ws), ws.numel(), st))
             else:
-                check(L.jamba_paged_extend_workspace_size(ctypes.byref(cfg), H, T, ctypes.byref(n)))
-            ws = torch.empty(max(n.value, 16), dtype=torch.uint8, device=q.device)
-            if q_start is None:
-                check(L.jamba_paged_decode(ctypes.byref(cfg), H, _p(q), ld, _p(k_pages), _p(v_pages), _p(table),
+                ws = torch.empty(cfg.workspace(index, "jamba_paged_extend_workspace_size", H, T), dtype=torch.uint8,
+                                 device=device)
+                check(L.jamba_paged_extend(cfg.ref, H, _p(q), ld, T, _p(q_start), _p(k_pages), _p(v_pages), _p(table),
                                            _p(lengths), _p(out), ld_o, _p(lse), _p(ws), ws.numel(), st))
-            else:
-                check(L.jamba_paged_extend(ctypes.byref(cfg), H, _p(q), ld, T, _p(q_start), _p(k_pages),
-                                           _p(v_pages), _p(table), _p(lengths), _p(out), ld_o, _p(lse), _p(ws),
-                                           ws.numel(), st))
-    return (out, lse) if want_lse else out
+        return (out, lse) if want_lse else out
+
+    return _run(index, stream, body, out)
 
 
 def paged_decode(q, k_pages, v_pages, table, lengths, out=None, want_lse=False, stream=None):
@@ -258,8 +308,11 @@ class PagedKVCache:
             if not 0 <= s < len(parent):
                 raise ValueError("slot %d is outside 0 .. %d" % (s, len(parent) - 1))
             parent[s] = -1
-        with _Call(self.table.device, stream):
-            self.fork(torch.tensor(parent, dtype=torch.int32, device=self.table.device), stream=stream)
+
+        def body(_):
+            self.fork(torch.tensor(parent, dtype=torch.int32, device=self.table.device))
+
+        _run(self.table.get_device(), stream, body)
 
     def grow(self, add, stream=None):
         """See pages_grow."""
@@ -270,7 +323,7 @@ class PagedKVCache:
         return pages_compact(self.data, self.refs, self.table, self.lengths, stream=stream)
 
     def config(self, layer):
-        """(jamba_pages_config of one layer, its keys, its values)."""
+        """(a layer's sizes, its keys, its values)."""
         if not 0 <= layer < self.layers:
             raise ValueError("layer %d is outside 0 .. %d" % (layer, self.layers - 1))
         _, N, G, P, _ = self.data.shape
