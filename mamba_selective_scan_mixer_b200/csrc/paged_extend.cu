@@ -797,36 +797,63 @@ paged_extend_join_kernel(const ExParams p) {
   while (c + parts < (int)gridDim.x && !p.meta[c + parts - 1].ends) ++parts;   // CTA c + i continues the unit; the last one ends it
   ExSeq q;
   q.load(p, me.s);
-#pragma unroll 1
+  // four rows at once, so that their loads are in flight together
+  const int rr = blockIdx.y * 32 + warp * 4, t = rr >> 7;
+  int tok[4];
+  bool in[4], any = false;
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int rr = blockIdx.y * 32 + warp * 4 + i, t = rr >> 7, r = rr & 127;
-    const int tok_r = r / p.rep, tok = (2 * me.u + t) * p.tpt + tok_r;
-    if (tok_r >= p.tpt || tok >= q.n) continue;
-    auto slot = [&](int k) { return (long long)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * 256 + rr; };
-    float mm = -INFINITY;
-    for (int k = 0; k < parts; ++k) mm = fmaxf(mm, p.part_ml[slot(k) * 2]);
-    float ls = 0.f;
-    float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(k) * 2);
-      const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot(k) * PG_D + lane * 4);
-      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
-      ls += ml.y * f;
-      os.x += x.x * f;
-      os.y += x.y * f;
-      os.z += x.z * f;
-      os.w += x.w * f;
+    const int tok_r = ((rr & 127) + i) / p.rep;
+    tok[i] = (2 * me.u + t) * p.tpt + tok_r;
+    in[i] = tok_r < p.tpt && tok[i] < q.n;
+    any = any || in[i];
+  }
+  if (!any) return;
+  float m[4], l[4];
+  float4 o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const long long row0 = (long long)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * 256 + rr;
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!in[i]) continue;
+      ml[i] = *reinterpret_cast<const float2*>(p.part_ml + (row0 + i) * 2);
+      x[i] = *reinterpret_cast<const float4*>(p.part_o + (row0 + i) * PG_D + lane * 4);
     }
-    const float inv = ls > 0.f ? 1.f / ls : 0.f;
-    const long long row = q.q0 + tok;
-    const int head = me.g * p.rep + r % p.rep;
-    __nv_bfloat162 h01 = __floats2bfloat162_rn(os.x * inv, os.y * inv), h23 = __floats2bfloat162_rn(os.z * inv, os.w * inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!in[i] || ml[i].x == -INFINITY) continue;   // a part whose keys the row does not see
+      const float mn = fmaxf(m[i], ml[i].x), fa = ex2(m[i] - mn), fb = ex2(ml[i].x - mn);
+      m[i] = mn;
+      l[i] = l[i] * fa + ml[i].y * fb;
+      o[i].x = o[i].x * fa + x[i].x * fb;
+      o[i].y = o[i].y * fa + x[i].y * fb;
+      o[i].z = o[i].z * fa + x[i].z * fb;
+      o[i].w = o[i].w * fa + x[i].w * fb;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!in[i]) continue;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    const long long row = q.q0 + tok[i];
+    const int head = me.g * p.rep + ((rr & 127) + i) % p.rep;
+    const __nv_bfloat162 h01 = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv);
+    const __nv_bfloat162 h23 = __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv);
     uint2 u;
-    u.x = *reinterpret_cast<uint32_t*>(&h01);
-    u.y = *reinterpret_cast<uint32_t*>(&h23);
+    u.x = *reinterpret_cast<const uint32_t*>(&h01);
+    u.y = *reinterpret_cast<const uint32_t*>(&h23);
     *reinterpret_cast<uint2*>(p.o + row * p.ld_o + (long long)head * PG_D + lane * 4) = u;
     if (p.lse && lane == 0)
-      p.lse[row * p.H + head] = ls > 0.f ? (mm + log2f(ls)) * 0.6931471805599453f : -INFINITY;
+      p.lse[row * p.H + head] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
   }
 }
 
