@@ -66,18 +66,18 @@ struct ExParams {
   int* err;
 };
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0 (Euclid-like reduction)
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+// sum over i < n of floor((a i + b) / m) (Euclid-like reduction); a n + b below 2^32
+__device__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   long long r = 0;
   while (n > 0) {
-    r += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+    r += (long long)(a / m) * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
     a %= m;
     b %= m;
-    const long long y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const long long t = a;
+    const uint32_t t = a;
     a = m;
     m = t;
   }
@@ -103,7 +103,7 @@ struct ExSeq {
   }
   // cost of the units before u (of one KV head)
   __device__ long long before(const ExParams& p, int u) const {
-    const long long tc = 2 * p.tpt, base = len - n;
+    const int tc = 2 * p.tpt, base = len - n;
     if (u <= 0) return 0;
     long long last = (long long)EX_UNIT_COST * u;
     if (u == units) {                            // the last unit may be short
@@ -111,11 +111,8 @@ struct ExSeq {
       --u;
     }
     // units 0 .. u-1 end at base + (i + 1) tc: ceil(x / 128) = floor((x + 127) / 128), 1 where x <= 0
-    long long ones = 0;
-    if (base < 0) {
-      ones = -base / tc;                         // units that end at or before position 0
-      if (ones > u) ones = u;
-    }
+    int ones = 0;
+    if (base < 0) ones = min(-base / tc, u);     // units that end at or before position 0
     return last + ones + floor_sum(u - ones, EX_BK, tc, base + (ones + 1) * tc + EX_BK - 1);
   }
   __device__ long long total(const ExParams& p) const { return units ? before(p, units) * p.g.G : 0; }
@@ -354,7 +351,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     const __grid_constant__ CUtensorMap tmV, const ExParams p) {
   using S = ExSmem;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long sh_left;
+  __shared__ long long sh_left, sh_rem;
   __shared__ int sh_pos[4];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);
@@ -437,15 +434,9 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           const long long head = t / p.g.G;
           const int g = (int)(rem / head);
           rem -= g * head;
-          int lo = 0, hi = q.units;              // before(lo) <= rem < before(hi)
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (q.before(p, mid) <= rem) lo = mid; else hi = mid;
-          }
           sh_pos[0] = s;
           sh_pos[1] = g;
-          sh_pos[2] = lo;
-          sh_pos[3] = (int)(rem - q.before(p, lo));
+          sh_rem = rem;
           break;
         }
         rem -= t;
@@ -454,6 +445,22 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     if (threadIdx.x == 0) sh_left = b - a;
   }
   fence_async_shared();                          // the sums' memory goes to the copies
+  __syncthreads();
+  if (warp == 0 && sh_left > 0) {                // the unit: before(lo) <= sh_rem < before(hi), 32 places at a time
+    ExSeq q;
+    q.load(p, sh_pos[0]);
+    int lo = 0, hi = q.units;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const uint32_t below = __ballot_sync(0xffffffffu, at < hi && q.before(p, at) <= sh_rem);
+      lo += (31 - __clz(below)) * step;          // lane 0's place is always below
+      hi = min(hi, lo + step);
+    }
+    if (lane == 0) {
+      sh_pos[2] = lo;
+      sh_pos[3] = (int)(sh_rem - q.before(p, lo));
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -660,19 +667,25 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         // The terms are formed against the reference from the blocks before, while this block's
         // maximum is found on the way; P replaces S only afterwards.  A reference up to 2^EX_REDO
         // too low does no harm (P and O have fp32's exponents): it is raised for the next block.
-        // Where it is lower still the warp forms the block again.
+        // Where it is further off the warp forms the block again.  A unit's first block takes 0, where no key is
+        // masked, and its maximum beforehand where some are (it may be that of none).
         uint32_t pk[32];
         float mx[2], sum[2];
-        if (kb == w.kb0) {
+        if (kb == w.kb0 && masked) {
           ex_row_max(tS, masked, lim, quad, mx);
           m[0] = mx[0] * p.sl2;
           m[1] = mx[1] * p.sl2;
         }
         ex_terms(tS, masked, lim, quad, m, p.sl2, pk, mx, sum);
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + EX_REDO || mx[1] > m[1] + EX_REDO)) {
+        // no reference yet (-inf): the terms were formed against 0
+        const bool far[2] = {mx[0] > (m[0] == -INFINITY ? 0.f : m[0]) + EX_REDO ||
+                                 (m[0] == -INFINITY && mx[0] < -EX_REDO && mx[0] > -INFINITY),
+                             mx[1] > (m[1] == -INFINITY ? 0.f : m[1]) + EX_REDO ||
+                                 (m[1] == -INFINITY && mx[1] < -EX_REDO && mx[1] > -INFINITY)};
+        if (__any_sync(0xffffffffu, far[0] || far[1])) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (mx[e] > m[e] + EX_REDO) {
+            if (far[e]) {
               const float corr = ex2(m[e] - mx[e]);
               l[e] *= corr;
               pend[e] *= corr;
@@ -681,6 +694,9 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
           }
           ex_terms(tS, masked, lim, quad, m, p.sl2, pk, mx, sum);
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (m[e] == -INFINITY && mx[e] > -INFINITY) m[e] = 0.f;
         // the product that wrote O last is done: S_j was issued after it
         if (kb > w.kb0 && __any_sync(0xffffffffu, pend[0] != 1.f || pend[1] != 1.f)) {
 #pragma unroll 1
@@ -723,7 +739,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const long long row = w.q.q0 + tok0 + tok_r[e];
-        const int head = w.g * p.rep + r[e] % p.rep;
+        const int head = w.g * p.rep + r[e] - tok_r[e] * p.rep;
         f[e] = whole ? (l[e] > 0.f ? pend[e] / l[e] : 0.f) : pend[e];
         dst[e] = p.o + row * p.ld_o + (long long)head * PG_D;
         pdst[e] = p.part_o + (part + r[e]) * PG_D;
