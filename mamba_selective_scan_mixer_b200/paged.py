@@ -238,7 +238,7 @@ def _attend(q, k_pages, v_pages, table, lengths, q_start, out, want_lse, stream)
     def body(st, out):
         L, device = lib(), q.device
         if out is None:
-            out = torch.empty((T, H, HEAD_DIM), dtype=_BF16, device=device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         ld_o = _rows(out, "out")[2]
         lse = torch.empty((T, H), dtype=torch.float32, device=device) if want_lse else None
         if T:
