@@ -589,7 +589,8 @@ jamba_status jamba_attn_step(const jamba_attn_config* cfg, const jamba_attn_weig
  * any length share one pool, prefixes are held once by several sequences, and
  * memory is taken and given back page by page (the serving form of the
  * attention layer's cache; the pages say nothing about the cache's layout).
- * All of it is device data, so every call can be captured into a CUDA graph.
+ * All of it is device data, so every call can be captured into a CUDA graph
+ * (after a first call on the device, which allocates the status word).
  *   data     [planes, num_pages, n_kv_heads, page_size, head_dim] dtype: the
  *            pool.  A plane is one array of pages (for instance the keys of
  *            layer l in plane 2l and its values in plane 2l + 1); a page

@@ -533,3 +533,107 @@ def test_binding_refusals(J):
         att.paged_step(x, cache)
     with pytest.raises(ValueError):
         att.paged_prefill(x, st, J.PagedKVCache(1, 4, 4, 2, 64))
+
+
+# ------------------------------------------------------------------- the rest
+
+def test_extend_rows_before_the_first_sequence_and_empty_sequences_with_tokens(J):
+    """q_start that begins at 2 (two rows that no sequence counts), a sequence whose tokens are
+    not in its length (0), a table with a row stride of its own."""
+    lengths, start = [40, 0, 150], [2, 9, 14, 34]
+    rng = np.random.default_rng(61)
+    k, v, table = _cache(rng, lengths, 2, 16)
+    wide = torch.full((3, table.shape[1] + 4), 77777, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = _i32(table)
+    t = wide[:, :table.shape[1]]
+    q = _q(36, 8, 2, 61)
+    out = torch.full((36, 8, 128), 7.0, dtype=BF, device="cuda")
+    got, lse = J.paged_extend(q, k.cuda(), v.cuda(), t, _i32(lengths), _i32(start), out=out, want_lse=True)
+    want = op.attention(to_np(q), to_np(k), to_np(v), table, np.array(lengths), start)
+    _check(got, lse, want)
+    assert (got[:2] == 7).all() and (got[34:] == 7).all()
+    assert (got[9:14] == 0).all() and torch.isneginf(lse[9:14]).all()
+    d = J.paged_decode(q[:3], k.cuda(), v.cuda(), t, _i32(lengths))
+    _check(d, None, op.attention(to_np(q[:3]), to_np(k), to_np(v), table, np.array(lengths), np.arange(4)))
+
+
+def test_pages_past_four_gigabytes(J):
+    """A plane of 9.2 GB: pages whose rows lie past 2^32 bytes (and 2^31 elements)."""
+    G, P, N = 8, 64, 70000
+    lengths, new = [300, 90], [70, 1]
+    kc, vc = (torch.empty(N, G, P, 128, dtype=BF, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(62)
+    k, v, small = _cache(rng, lengths, G, P, spare=0)
+    k.nan_to_num_(0.0)
+    v.nan_to_num_(0.0)
+    pages = np.concatenate([small[0, :5], small[1, :2]])
+    where = {int(p): N - 1 - 3 * i for i, p in enumerate(pages)}
+    table = np.full_like(small, -1)
+    table[0, :5], table[1, :2] = [where[int(p)] for p in small[0, :5]], [where[int(p)] for p in small[1, :2]]
+    at = torch.tensor([where[int(p)] for p in pages], device="cuda")
+    kc[at], vc[at] = k[pages].cuda(), v[pages].cuda()
+    q = _q(71, 32, G, 62)
+    start = [0, 70, 71]
+    rows = _q(71, 2 * G, G, 63)
+    J.paged_append(rows[:, :G], rows[:, G:], kc, vc, _i32(table), _i32(lengths), _i32(start))
+    kn, vn = k.float().numpy(), v.float().numpy()
+    op.append(rows[:, :G].float().cpu().numpy(), rows[:, G:].float().cpu().numpy(), kn, vn, small, lengths, start)
+    np.testing.assert_array_equal(kc[at].float().cpu().numpy(), kn[pages])
+    want = op.attention(to_np(q), kn.astype(np.float64), vn.astype(np.float64), small, np.array(lengths), start)
+    got, lse = J.paged_extend(q, kc, vc, _i32(table), _i32(lengths), _i32(start), want_lse=True)
+    _check(got, lse, want)
+    last = q[[69, 70]]
+    d, dl = J.paged_decode(last, kc, vc, _i32(table), _i32(lengths), want_lse=True)
+    _check(d, dl, {n: x[[69, 70]] for n, x in want.items()})
+    # compaction from the far end to the front, and a copied last page
+    data = torch.stack([kc[-64:], vc[-64:]])
+    del kc, vc
+    big = torch.empty(2, N // 2, G, P, 128, dtype=BF, device="cuda")
+    big[:, -64:] = data
+    refs = torch.zeros(N // 2, dtype=torch.int32, device="cuda")
+    t = _i32(np.where(table >= 0, table - N + N // 2, -1))
+    refs[t[t >= 0].long()] = 1
+    ln = _i32(lengths)
+    remap = J.pages_compact(big, refs, t, ln)
+    assert sorted(remap[remap >= 0].tolist()) == list(range(7)) and int(refs.sum()) == 7
+    back = torch.stack([big[0][t[0, :5].long()], big[1][t[0, :5].long()]])
+    np.testing.assert_array_equal(back.float().cpu().numpy(), np.stack([kn[small[0, :5]], vn[small[0, :5]]]))
+
+
+def test_upkeep_in_a_graph(J):
+    """fork, grow and compact captured once: every replay does the turn on what it finds."""
+    S, W, N, P = 4, 6, 40, 16
+    data = torch.randn(2, N, 1, P, 128, generator=torch.Generator().manual_seed(3)).to(BF)
+    d_o = data.float().numpy().copy()
+    refs, table, lengths = np.zeros(N, dtype=int), np.full((S, W), -1), np.zeros(S, dtype=int)
+    d, r, t, ln = data.cuda(), _i32(refs), _i32(table), _i32(lengths)
+    parent, add = np.array([0, 0, -1, 2]), np.array([5, 20, 33, 1])
+    pg, ag = _i32(parent), _i32(add)
+    J.device_status()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        J.pages_fork(pg, r, t, ln, P)
+        granted = J.pages_grow(ag, d, r, t, ln)
+        remap = J.pages_compact(d, r, t, ln)
+    for _ in range(8):
+        graph.replay()
+        op.fork(parent, refs, table, lengths, P)
+        want = op.grow(add, d_o, refs, table, lengths)
+        moved = op.compact(d_o, refs, table, lengths)
+        assert granted.tolist() == want
+        for got, exp in ((t, table), (r, refs), (ln, lengths), (remap, moved)):
+            np.testing.assert_array_equal(got.cpu().numpy(), exp)
+        np.testing.assert_array_equal(d.float().cpu().numpy(), d_o)
+
+
+def test_sequences_that_share_pages(J):
+    """Two slots that hold the same pages see the same keys; a third its own length of them."""
+    lengths = [200, 200, 77]
+    rng = np.random.default_rng(64)
+    k, v, table = _cache(rng, [200], 2, 32)
+    table = np.repeat(table, 3, axis=0)
+    q = _q(3, 8, 2, 64)
+    q = q[[0, 0, 2]]
+    got, lse = J.paged_decode(q, k.cuda(), v.cuda(), _i32(table), _i32(lengths), want_lse=True)
+    _check(got, lse, op.attention(to_np(q), to_np(k), to_np(v), table, np.array(lengths), np.arange(4)))
+    assert torch.equal(got[0], got[1])
