@@ -30,7 +30,7 @@ namespace jb {
 constexpr int DP_BK = 64;                        // positions per block
 constexpr int DP_THREADS = 160;                  // 4 consumer warps, 1 producer
 constexpr int DP_CTAS = 2;                       // per SM
-constexpr int DP_MIN_BLOCKS = 2;                 // of a CTA's range
+constexpr int DP_WHOLE = 4;                      // blocks of a unit that is not worth cutting
 
 template <int NT> struct DpSmem {                // NT: tiles of eight query heads
   static constexpr int STAGES = NT == 1 ? 3 : 2;
@@ -160,8 +160,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       if (i < warp) before += sh_warp[i];
       N += sh_warp[i];
     }
-    long long per = (N + gridDim.x - 1) / gridDim.x;
-    if (per < DP_MIN_BLOCKS) per = DP_MIN_BLOCKS;
+    // With few blocks, ranges of a unit up to DP_WHOLE blocks, of two blocks beyond: a block more costs a CTA 0.5 us, joining
+    // parts 1 to 2 us (one sequence of 64 tokens whole 5.9 us, two of its heads in one range 7.4 us; of 500 tokens whole
+    // 9.5 us, in four parts 8.1 us; of 1000 tokens whole 13.3 us, in eight parts 9.5 us)
+    const long long units = (long long)p.g.S * p.g.G, mean = (N + units - 1) / units;
+    const long long per = max((N + gridDim.x - 1) / gridDim.x, mean <= DP_WHOLE ? mean : 2);
     const long long a = min(N, blockIdx.x * per), b = min(N, a + per);
     if (b > a && a >= before && a < before + sum) {
       long long rem = a - before;
@@ -481,8 +484,8 @@ paged_decode_join_kernel(const DpParams p, int ctas) {
 // CTAs: no more than the blocks that the table can hold
 static int decode_grid(const PageGeom& g) {
   const long long most = (long long)g.S * g.G * ((((long long)g.max_pages << g.shift) + DP_BK - 1) / DP_BK);
-  const long long ctas = (most + DP_MIN_BLOCKS - 1) / DP_MIN_BLOCKS, full = (long long)DP_CTAS * num_sms();
-  return (int)(ctas < full ? ctas : full);
+  const long long full = (long long)DP_CTAS * num_sms();
+  return (int)(most < full ? most : full);
 }
 static size_t decode_meta_bytes(int grid) { return ((size_t)grid * sizeof(DpMeta) + 255) & ~size_t(255); }
 
