@@ -700,7 +700,10 @@ jamba_status jamba_paged_decode(const jamba_pages_config* cfg, int n_heads, cons
  *   q, o, lse as in jamba_paged_decode with `tokens` rows; q_start as in
  *   jamba_paged_append (required)
  * A token before position 0 gets o = 0 and lse = -inf; rows of q past
- * q_start[max_seqs] are left out.  At most 128 query heads per KV head.
+ * q_start[max_seqs] are left out.  A key that is not finite reaches the tokens that
+ * see it, a value that is not finite any new token of its sequence (it enters the
+ * products of earlier ones with weight 0), neither another sequence.  At most 128
+ * query heads per KV head.
  * Errors as jamba_paged_decode. */
 jamba_status jamba_paged_extend(const jamba_pages_config* cfg, int n_heads, const void* q, int ld_q, int tokens,
                                 const int32_t* q_start, const void* k_pages, const void* v_pages,

@@ -63,10 +63,13 @@ jamba_status check_planes(const jamba_pages_config* c) {
 }
 
 jamba_status check_heads(const PageGeom& g, int n_heads, int tokens, int max_rep) {
-  if (n_heads <= 0 || n_heads % g.G) return fail(JAMBA_ERR_INVALID_ARG, "paged attention: n_kv_heads must divide n_heads");
+  if (n_heads <= 0 || n_heads % g.G)
+    return fail(JAMBA_ERR_INVALID_ARG, "paged attention: n_kv_heads must divide n_heads");
   if (n_heads / g.G > max_rep)
-    return fail(JAMBA_ERR_UNSUPPORTED, "paged attention: at most " + std::to_string(max_rep) + " query heads per KV head");
-  if ((long long)tokens * n_heads > INT_MAX) return fail(JAMBA_ERR_UNSUPPORTED, "paged attention: tokens * heads above 2^31 - 1");
+    return fail(JAMBA_ERR_UNSUPPORTED,
+                "paged attention: at most " + std::to_string(max_rep) + " query heads per KV head");
+  if ((long long)tokens * n_heads > INT_MAX)
+    return fail(JAMBA_ERR_UNSUPPORTED, "paged attention: tokens * heads above 2^31 - 1");
   return JAMBA_OK;
 }
 

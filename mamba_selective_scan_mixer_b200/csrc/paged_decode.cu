@@ -160,9 +160,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       if (i < warp) before += sh_warp[i];
       N += sh_warp[i];
     }
-    // With few blocks, ranges of a unit up to DP_WHOLE blocks, of two blocks beyond: a block more costs a CTA 0.5 us, joining
-    // parts 1 to 2 us (one sequence of 64 tokens whole 5.9 us, two of its heads in one range 7.4 us; of 500 tokens whole
-    // 9.5 us, in four parts 8.1 us; of 1000 tokens whole 13.3 us, in eight parts 9.5 us)
+    // With few blocks, ranges of a unit up to DP_WHOLE blocks, of two blocks beyond: a block more costs
+    // a CTA 0.5 us, joining parts 1 to 2 us (one sequence of 64 tokens whole 5.9 us, two of its heads in
+    // one range 7.4 us; of 500 tokens whole 9.5 us, in four parts 8.1 us; of 1000 tokens whole 13.3 us,
+    // in eight parts 9.5 us)
     const long long units = (long long)p.g.S * p.g.G, mean = (N + units - 1) / units;
     const long long per = max((N + gridDim.x - 1) / gridDim.x, mean <= DP_WHOLE ? mean : 2);
     const long long a = min(N, blockIdx.x * per), b = min(N, a + per);
@@ -325,10 +326,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
               float mx = fmaxf(s0, s8);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              const float mn = fmaxf(m[n][e], mx);           // the warp's first position is in
-              corr[e] = ex2(m[n][e] - mn);
-              pr[e] = ex2(s0 - mn);
-              pr[2 + e] = ex2(s8 - mn);
+              const float mn = fmaxf(m[n][e], mx);
+              const float ref = mn == -INFINITY ? 0.f : mn;  // so far every score is -inf: their terms are 0
+              corr[e] = ex2(m[n][e] - ref);
+              pr[e] = ex2(s0 - ref);
+              pr[2 + e] = ex2(s8 - ref);
               l[n][e] = l[n][e] * corr[e] + pr[e] + pr[2 + e];
               m[n][e] = mn;
             }
@@ -344,7 +346,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
 #pragma unroll
             for (int h = 0; h < 2; ++h) {        // positions gq, gq + 8: transposed to positions 2 tq, 2 tq + 1 (+ 8)
               const __nv_bfloat162 hi = __floats2bfloat162_rn(pr[2 * h], pr[2 * h + 1]);
-              const __nv_bfloat162 lo = __floats2bfloat162_rn(pr[2 * h] - __low2float(hi), pr[2 * h + 1] - __high2float(hi));
+              const __nv_bfloat162 lo =
+                  __floats2bfloat162_rn(pr[2 * h] - __low2float(hi), pr[2 * h + 1] - __high2float(hi));
               ph[n][h] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&hi));
               pl[n][h] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&lo));
             }
@@ -425,7 +428,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             if (h >= p.rep) continue;
             const int head = w.g * p.rep + h;
             if (whole) {
-              const float inv = l[n][e] > 0.f ? 1.f / l[n][e] : 0.f;
+              const float inv = l[n][e] != 0.f ? 1.f / l[n][e] : 0.f;   // a NaN stays one
               bf16* dst = p.o + row * p.ld_o + (long long)head * PG_D;
 #pragma unroll
               for (int mm = 0; mm < 8; ++mm) {
@@ -434,7 +437,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
               }
               if (p.lse && gq == 0)
                 p.lse[row * p.H + head] =
-                    l[n][e] > 0.f ? (m[n][e] + log2f(l[n][e])) * 0.6931471805599453f : -INFINITY;
+                    l[n][e] != 0.f ? (m[n][e] + log2f(l[n][e])) * 0.6931471805599453f : -INFINITY;
             } else {
               float* dst = p.part + ((long long)(2 * blockIdx.x + (w.kb0 == 0)) * p.rep + h) * (PG_D + 2);
 #pragma unroll
@@ -463,7 +466,7 @@ paged_decode_join_kernel(const DpParams p, int ctas) {
   const DpMeta me = p.meta[c];
   if (!me.tail) return;
   int parts = 2;
-  while (c + parts < ctas && !p.meta[c + parts - 1].ends) ++parts;   // CTA c + i continues the unit; the last one ends it
+  while (c + parts < ctas && !p.meta[c + parts - 1].ends) ++parts;   // CTA c + i continues the unit, the last ends it
   auto src = [&](int k) { return p.part + ((long long)(k == 0 ? 2 * c + 1 : 2 * (c + k)) * p.rep + h) * (PG_D + 2); };
   float m = -INFINITY;
   for (int k = 0; k < parts; ++k) m = fmaxf(m, src(k)[PG_D]);
@@ -476,9 +479,9 @@ paged_decode_join_kernel(const DpParams p, int ctas) {
     o += x[d] * f;
   }
   const int head = me.g * p.rep + h;
-  p.o[me.s * p.ld_o + (long long)head * PG_D + d] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+  p.o[me.s * p.ld_o + (long long)head * PG_D + d] = __float2bfloat16_rn(l != 0.f ? o / l : 0.f);
   if (p.lse && d == 0)
-    p.lse[(long long)me.s * p.H + head] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    p.lse[(long long)me.s * p.H + head] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // CTAs: no more than the blocks that the table can hold
@@ -495,7 +498,8 @@ size_t paged_decode_workspace_bytes(const PageGeom& g, int H) {
 }
 
 template <int NT>
-static jamba_status launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const DpParams& p, int grid, cudaStream_t s) {
+static jamba_status launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const DpParams& p, int grid,
+                                  cudaStream_t s) {
   static std::atomic<bool> configured[64];
   int dev = 0;
   JB_CUDA(cudaGetDevice(&dev));

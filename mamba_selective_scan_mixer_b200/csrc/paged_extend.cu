@@ -37,7 +37,7 @@ constexpr int EX_BK = 128;                       // keys per block
 constexpr int EX_SLOTS = 5;                      // ring of K and V blocks
 constexpr int EX_THREADS = 640;                  // producer, an MMA warp per tile, V tails, 8 + 8 softmax warps
 constexpr int EX_MIN_COST = 4;                   // of a CTA's range
-constexpr int EX_UNIT_COST = 2;                  // what a unit costs beyond its blocks (Q, first maximum, output), in blocks
+constexpr int EX_UNIT_COST = 2;                  // what a unit costs beyond its blocks (Q, output), in blocks
 
 struct ExSmem {
   static constexpr uint32_t SUB = 128 * 128;     // 128 rows x 64 bf16, swizzled
@@ -123,7 +123,7 @@ struct ExSeq {
 struct ExWalk {
   ExSeq q;
   int s, g, u, kb0, kb1, nb;                     // nb: blocks of the unit
-  long long at, left;                            // step of the unit that the item starts at; steps of the range from there on
+  long long at, left;                            // step of the unit at the item's start, steps of the range from there
   __device__ bool open(const ExParams& p) {      // the item at (s, g, u, at); false: no block is left
     if (left <= 0) return false;
     nb = q.blocks(p, u);
@@ -170,9 +170,9 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, float (&v)[16]) 
 __device__ __forceinline__ void tmem_st_16x256b(uint32_t taddr, const float (&v)[16]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, const uint32_t (&r)[32]) {   // 64 columns
@@ -197,6 +197,11 @@ __device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float nan_max(float a, float b) {   // NaN where either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
 __device__ __forceinline__ float quad_max(float v) {
@@ -234,14 +239,13 @@ constexpr float EXC0 = 0.99999926144f, EXC1 = 0.69312181475f, EXC2 = 0.240247448
 
 // 2^x for both halves on the FMA pipe, x in [-126, 126] (lower ones count as -126): the nearest
 // integer n through the mantissa of x + 1.5 2^23, a degree-4 polynomial for 2^f with f = x - n in
-// [-1/2, 1/2] (fitted for the least largest
-// relative error, 2.6e-6; P keeps 2^-9), and n
-// added to its exponent.  Takes some of the terms because ex2 alone runs at 16 a cycle and SM: 128 x 256
-// terms take the 2048 cycles that their four products take.
+// [-1/2, 1/2] (fitted for the least largest relative error, 2.6e-6; P keeps 2^-9), and n added to its
+// exponent; a NaN comes out as one or above 2^126.  Takes some of the terms because ex2 alone runs at
+// 16 a cycle and SM: 128 x 256 terms take the 2048 cycles that their four products take.
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
   const float big = 12582912.f;
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
+  x.x = nan_max(x.x, -126.f);
+  x.y = nan_max(x.y, -126.f);
   const float2 one = make_float2(1.f, 1.f);
   const float2 t = ffma2(x, one, make_float2(big, big));
   const float2 n = ffma2(t, one, make_float2(-big, -big));
@@ -281,7 +285,7 @@ __device__ __forceinline__ void ex_terms_t(uint32_t tS, const int (&lim)[2], int
       mx[e] = max3(mx[e], a, b);
       const float2 x = ffma2(make_float2(a, b), sl, make_float2(ref[e], ref[e]));
       float2 t;
-      if (!MASKED && i % EX_FMA_EVERY == EX_FMA_EVERY - 1 - (c & 1))   // masked scores are -inf: their terms are exactly 0
+      if (!MASKED && i % EX_FMA_EVERY == EX_FMA_EVERY - 1 - (c & 1))   // masked scores: their terms are exactly 0
         t = ex2_fma(x);
       else
         t = make_float2(ex2(x.x), ex2(x.y));
@@ -716,7 +720,8 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         if (lane == 0) mbar_arrive(P_FULL(t));
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          l[e] += sum[e];
+          // a NaN that went through ex2_fma is one again (terms end at 2^EX_REDO), a block of -inf adds nothing
+          l[e] += mx[e] == -INFINITY ? 0.f : sum[e] < 0x1p100f ? sum[e] : NAN;
           pend[e] = 1.f;
           if (mx[e] > m[e] + EX_RAISE) {
             pend[e] = ex2(m[e] - mx[e]);
@@ -732,7 +737,8 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       ++no;
       if (!ok) break;
       tc_fence_after();
-      const long long part = ((long long)(2 * blockIdx.x + (w.kb0 == 0)) * 2 + t) * 128;   // continued: 0, begun here: 1
+      // a CTA's parts: 0 continues a unit, 1 begins one
+      const long long part = ((long long)(2 * blockIdx.x + (w.kb0 == 0)) * 2 + t) * 128;
       float f[2];
       bf16* dst[2];
       float* pdst[2];
@@ -740,14 +746,14 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       for (int e = 0; e < 2; ++e) {
         const long long row = w.q.q0 + tok0 + tok_r[e];
         const int head = w.g * p.rep + r[e] - tok_r[e] * p.rep;
-        f[e] = whole ? (l[e] > 0.f ? pend[e] / l[e] : 0.f) : pend[e];
+        f[e] = whole ? (l[e] != 0.f ? pend[e] / l[e] : 0.f) : pend[e];
         dst[e] = p.o + row * p.ld_o + (long long)head * PG_D;
         pdst[e] = p.part_o + (part + r[e]) * PG_D;
         if (row_in[e] && quad == 0) {
           if (!whole)
             *reinterpret_cast<float2*>(p.part_ml + (part + r[e]) * 2) = make_float2(m[e], l[e]);
           else if (p.lse)
-            p.lse[row * p.H + head] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.6931471805599453f : -INFINITY;
+            p.lse[row * p.H + head] = l[e] != 0.f ? (m[e] + log2f(l[e])) * 0.6931471805599453f : -INFINITY;
         }
       }
 #pragma unroll 1
@@ -810,7 +816,8 @@ paged_extend_join_kernel(const ExParams p) {
   const ExMeta me = p.meta[c];
   if (!me.tail) return;
   int parts = 2;
-  while (c + parts < (int)gridDim.x && !p.meta[c + parts - 1].ends) ++parts;   // CTA c + i continues the unit; the last one ends it
+  // CTA c + i continues the unit, the last one ends it
+  while (c + parts < (int)gridDim.x && !p.meta[c + parts - 1].ends) ++parts;
   ExSeq q;
   q.load(p, me.s);
   // four rows at once, so that their loads are in flight together
@@ -846,7 +853,7 @@ paged_extend_join_kernel(const ExParams p) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (!in[i] || ml[i].x == -INFINITY) continue;   // a part whose keys the row does not see
+      if (!in[i] || ml[i].y == 0.f) continue;   // a part whose keys the row does not see
       const float mn = fmaxf(m[i], ml[i].x), fa = ex2(m[i] - mn), fb = ex2(ml[i].x - mn);
       m[i] = mn;
       l[i] = l[i] * fa + ml[i].y * fb;
@@ -859,7 +866,7 @@ paged_extend_join_kernel(const ExParams p) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (!in[i]) continue;
-    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    const float inv = l[i] != 0.f ? 1.f / l[i] : 0.f;
     const long long row = q.q0 + tok[i];
     const int head = me.g * p.rep + ((rr & 127) + i) % p.rep;
     const __nv_bfloat162 h01 = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv);
@@ -869,7 +876,7 @@ paged_extend_join_kernel(const ExParams p) {
     u.y = *reinterpret_cast<const uint32_t*>(&h23);
     *reinterpret_cast<uint2*>(p.o + row * p.ld_o + (long long)head * PG_D + lane * 4) = u;
     if (p.lse && lane == 0)
-      p.lse[row * p.H + head] = l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+      p.lse[row * p.H + head] = l[i] != 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -916,9 +923,9 @@ jamba_status paged_extend(const PageGeom& g, int H, const void* q, long long ld_
   static std::atomic<bool> configured[64];
   int dev = 0;
   JB_CUDA(cudaGetDevice(&dev));
-  if (dev < 64 && !configured[dev]) {
+  if (dev >= 64 || !configured[dev]) {
     JB_CUDA(cudaFuncSetAttribute(paged_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ExSmem::BYTES));
-    configured[dev] = true;
+    if (dev < 64) configured[dev] = true;
   }
   JB_CUDA(launch_pdl(paged_extend_kernel, dim3(grid), dim3(EX_THREADS), ExSmem::BYTES, s, mq, mk, mv, p));
   JB_CUDA(launch_pdl(paged_extend_join_kernel, dim3(grid, 8), dim3(256), 0, s, p));

@@ -101,7 +101,8 @@ pages_fork_small_kernel(PageGeom g, const int* __restrict__ parent, int* refs, i
   int entry = -2, len = -2;      // -2: nothing to write
   if (i < g.S) {
     const int p = parent[i];
-    if (p != i && checked(p >= -1 && p < g.S, err) && p >= -1 && p < g.S) len = p >= 0 ? clamp_len(g, lengths[p], err) : 0;
+    if (p != i && checked(p >= -1 && p < g.S, err) && p >= -1 && p < g.S)
+      len = p >= 0 ? clamp_len(g, lengths[p], err) : 0;
   }
   if (s < g.S) {
     const int p = parent[s];

@@ -637,3 +637,59 @@ def test_sequences_that_share_pages(J):
     got, lse = J.paged_decode(q, k.cuda(), v.cuda(), _i32(table), _i32(lengths), want_lse=True)
     _check(got, lse, op.attention(to_np(q), to_np(k), to_np(v), table, np.array(lengths), np.arange(4)))
     assert torch.equal(got[0], got[1])
+
+
+def test_scores_that_are_not_finite(J):
+    """A NaN in a key makes exactly the (token, head) pairs that see it NaN, in sequences that one
+    CTA takes and in ones that are cut into parts; keys of -inf (scores of -inf, over whole warps' and
+    blocks' positions) have no weight, and where every score is -inf the output is 0 and lse -inf."""
+    G, H, P = 2, 8, 32
+    rng = np.random.default_rng(71)
+    lengths = [40, 1500, 90, 700, 300]
+    k, v, table = _cache(rng, lengths, G, P)
+
+    def key(s, g, pos):
+        return k[table[s, pos // P], g, pos % P]
+
+    new = [3, 300, 1, 2, 300]
+    qs = np.concatenate([[0], np.cumsum(new)])
+    q = _q(qs[-1], H, G, 71)
+    q[:, :, 0] = q[:, :, 0].abs() + 0.25           # against -inf in a key: a score of -inf
+    bad = {(0, 0): 5, (1, 1): 1251, (3, 0): 699}   # (sequence, KV head): position
+    for (s, g), pos in bad.items():
+        key(s, g, pos)[7] = NAN
+    for pos in list(range(0, 256)) + list(range(272, 288)) + [1499]:
+        key(1, 0, pos)[0] = -float("inf")
+    for pos in range(90):
+        key(2, 1, pos)[0] = -float("inf")
+    for pos in range(300):
+        key(4, 0, pos)[0] = -float("inf")
+    kc, vc, tab, lens = k.cuda(), v.cuda(), _i32(table), _i32(lengths)
+    ko = to_np(k)
+    for (s, g), pos in bad.items():                # the oracle's own answer where nothing is NaN
+        ko[table[s, pos // P], g, pos % P, 7] = 0.0
+    rep = H // G
+    for ragged in (False, True):
+        start = qs if ragged else np.arange(len(lengths) + 1)
+        rows = np.arange(qs[-1]) if ragged else qs[1:] - 1
+        qq = q[torch.tensor(rows, device="cuda")] if not ragged else q
+        if ragged:
+            got, lse = J.paged_extend(qq, kc, vc, tab, lens, _i32(start), want_lse=True)
+        else:
+            got, lse = J.paged_decode(qq, kc, vc, tab, lens, want_lse=True)
+        with np.errstate(invalid="ignore"):
+            want = op.attention(to_np(qq), ko, to_np(v), table, np.array(lengths), start)
+        o, z = to_np(got), to_np(lse)
+        for s, n in enumerate(lengths):
+            for t in range(start[s], start[s + 1]):
+                pos = n - start[s + 1] + t
+                for h in range(H):
+                    g = h // rep
+                    if bad.get((s, g), n) <= pos:
+                        assert np.isnan(o[t, h]).all() and np.isnan(z[t, h]), (ragged, s, t, h)
+                    elif (s, g) in ((2, 1), (4, 0)):
+                        assert (o[t, h] == 0).all() and np.isneginf(z[t, h]), (ragged, s, t, h)
+                    else:
+                        err = np.abs(o[t, h] - want["o"][t, h])
+                        assert (err <= TOL_O * want["spread"][t, h]).all(), (ragged, s, t, h)
+                        assert abs(z[t, h] - want["lse"][t, h]) <= 2.0 ** -12 + 2.0 ** -22 * abs(want["lse"][t, h])
