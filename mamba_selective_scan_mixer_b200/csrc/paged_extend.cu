@@ -22,21 +22,22 @@
 // tiles take turns at the tensor core (O_A += P_A V_j and S_A(j+1), then the same of B), each issued
 // by a warp of its own, and one tile's softmax runs under the other's products.  One softmax
 // reference per row: terms are formed against the one from the blocks before (0 for a first block
-// without a mask) while this block's maximum is found on the way, so scores are read once; it is
-// raised for the next block when a maximum passed it by more than 2^8, and O is then rescaled in
-// tensor memory.  Rows of V behind the sequence's last token are zeroed in shared memory, their
-// memory may hold anything.
+// without a mask), so scores are read once and no maximum is looked for; when a row's terms add up to
+// more than 2^16 it is raised for the next block, by a power of two, and O is then rescaled in tensor
+// memory.  Rows of V behind the sequence's last token are zeroed in shared memory, their memory may
+// hold anything.
 //
 // Rounding: P is bf16 (the tensor core's type; the sum is taken before), o is rounded once from fp32.
 //
 // Bounds: chunks by the tensor core and the softmax it waits for.  4096 tokens behind 12288, 32 heads
-// on 8: 0.96 ms, 1.0 PFLOP/s, 0.61 of the burst rate and 0.74 of the sustained one (the card holds
-// 1.55 to 1.65 GHz under it): a pair of blocks takes about 3600 cycles, its four products 2048, the
-// rest is the chain softmax (1600) -> products (1024) -> the next wait.  Measured there: without turns
-// 1.07 ms; P handed over in halves 1.03 ms; 64-key blocks with two score buffers a tile 1.18 ms; all
-// 16 warps on one tile's softmax 1.20 ms.  One warp issuing for both tiles took 0.90 ms, but 0.245 ms
-// for 24 sequences of 1 to 1500 tokens behind up to 6000 that take 0.147 ms so.  A few drafted
-// tokens (32 sequences of 5 behind 300 to 4096): 60 us, by the latency of a block, at half the rate
+// on 8: 0.87 ms, 1.1 PFLOP/s, 0.67 of the burst rate and 0.82 of the sustained one (the card holds
+// 1.55 to 1.65 GHz under it): a pair of blocks takes about 3600 cycles, its four products 2500 with
+// the shared memory's other traffic, the rest is the chain softmax (1600) -> products (1270) -> the
+// next wait.  Measured there: a maximum taken of every block and the reference raised from 2^8 on
+// 0.95 ms; before that without turns 1.07 ms; P handed over in halves 1.03 ms; 64-key blocks with two
+// score buffers a tile 1.18 ms; all 16 warps on one tile's softmax 1.20 ms.  24 sequences of 1 to 1500
+// tokens behind up to 6000: 0.142 ms (one warp issuing for both tiles 0.245 ms).  A few drafted
+// tokens (32 sequences of 5 behind 300 to 4096): 57 us, by the latency of a block, at half the rate
 // that reading their pages allows.  Every wait is bounded (see common.cuh).
 #include <climits>
 
@@ -164,8 +165,10 @@ struct ExWalk {
   }
 };
 
-constexpr float EX_RAISE = 8.f;    // log2 units: the reference is raised when a maximum passes it by more
-constexpr float EX_REDO = 64.f;    // ... and the block is formed again when by more than this
+// a row's terms in one block add up to more than this: the reference is raised, to even the exponents
+constexpr float EX_MAX_SUM = 0x1p16f;
+// ... to more than this, or to less than EX_MIN_SUM in a first block: the block is formed again
+constexpr float EX_FAR = 0x1p64f, EX_MIN_SUM = 0x1p-64f;
 
 // Softmax warps hold 16 rows of a tile each: in tcgen05.ld / st .16x256b and .16x128b a row's columns
 // lie over the four lanes of a quad (lane i: rows i / 4 and i / 4 + 8; of each 8 columns of 32
@@ -206,11 +209,6 @@ __device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
                :
                : "memory");
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 __device__ __forceinline__ float nan_max(float a, float b) {   // NaN where either is
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -245,7 +243,7 @@ __device__ __forceinline__ void ex_row_max(uint32_t tS, bool masked, const int (
   mx[1] = quad_max(mx[1]);
 }
 
-constexpr int EX_FMA_EVERY = 8;    // of the pairs of terms, one in so many goes to ex2_fma
+constexpr int EX_FMA_EVERY = 4;    // of the pairs of terms, one in so many goes to ex2_fma
 constexpr float EXC0 = 0.99999926144f, EXC1 = 0.69312181475f, EXC2 = 0.24024744849f, EXC3 = 0.05591786025f,
                 EXC4 = 0.00957010107f;
 
@@ -271,14 +269,13 @@ __device__ __forceinline__ float2 ex2_fma(float2 x) {
                      __int_as_float(__float_as_int(y.y) + (__float_as_int(t.y) << 23)));
 }
 
-// The terms 2^(s sl2 + ref) of the thread's two rows in bf16 pairs, their sums (before rounding, the thread's own
-// columns only) and the rows' largest scores.
+// The terms 2^(s sl2 + ref) of the thread's two rows in bf16 pairs, and their sums (before rounding) over the
+// thread's own columns.
 template <bool MASKED>
 __device__ __forceinline__ void ex_terms_t(uint32_t tS, const int (&lim)[2], int quad, const float (&ref)[2], float sl2,
-                                           uint32_t (&pk)[32], float (&mx)[2], float (&sum)[2]) {
+                                           uint32_t (&pk)[32], float (&sum)[2]) {
   const float2 sl = make_float2(sl2, sl2);
   float2 sm[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  mx[0] = mx[1] = -INFINITY;
   float s[2][16];
   tmem_ld_16x256b(tS, s[0]);
 #pragma unroll
@@ -294,7 +291,6 @@ __device__ __forceinline__ void ex_terms_t(uint32_t tS, const int (&lim)[2], int
         if (chunk_col(c, 2 * i, quad) > lim[e]) a = -INFINITY;
         if (chunk_col(c, 2 * i + 1, quad) > lim[e]) b = -INFINITY;
       }
-      mx[e] = max3(mx[e], a, b);
       const float2 x = ffma2(make_float2(a, b), sl, make_float2(ref[e], ref[e]));
       float2 t;
       if (!MASKED && i % EX_FMA_EVERY == EX_FMA_EVERY - 1 - (c & 1))   // masked scores: their terms are exactly 0
@@ -307,20 +303,15 @@ __device__ __forceinline__ void ex_terms_t(uint32_t tS, const int (&lim)[2], int
     }
   }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    mx[e] = quad_max(mx[e]);
-    sum[e] = sm[e].x + sm[e].y;
-  }
+  for (int e = 0; e < 2; ++e) sum[e] = sm[e].x + sm[e].y;
 }
 __device__ __forceinline__ void ex_terms(uint32_t tS, bool masked, const int (&lim)[2], int quad, const float (&m)[2],
-                                         float sl2, uint32_t (&pk)[32], float (&mx)[2], float (&sum)[2]) {
+                                         float sl2, uint32_t (&pk)[32], float (&sum)[2]) {
   const float ref[2] = {m[0] == -INFINITY ? 0.f : -m[0], m[1] == -INFINITY ? 0.f : -m[1]};
   if (masked)
-    ex_terms_t<true>(tS, lim, quad, ref, sl2, pk, mx, sum);
+    ex_terms_t<true>(tS, lim, quad, ref, sl2, pk, sum);
   else
-    ex_terms_t<false>(tS, lim, quad, ref, sl2, pk, mx, sum);
-  mx[0] *= sl2;
-  mx[1] *= sl2;
+    ex_terms_t<false>(tS, lim, quad, ref, sl2, pk, sum);
 }
 // w[g] of lane l of a quad becomes w[l] of lane g
 __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int quad) {
@@ -375,13 +366,12 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
   const uint32_t q_full = smem_u32(bars), q_empty = smem_u32(bars + 1);
   const uint32_t kv_full0 = smem_u32(bars + 2), kv_empty0 = smem_u32(bars + 2 + EX_SLOTS);
   const uint32_t land0 = smem_u32(bars + 2 + 2 * EX_SLOTS);   // a V block with rows to be zeroed has landed
-  const uint32_t tb0 = smem_u32(bars + 2 + 3 * EX_SLOTS);     // per tile: S full, P full, O full, drained, turn
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 12 + 3 * EX_SLOTS);
-#define S_FULL(t) (tb0 + 40 * (t))
-#define P_FULL(t) (tb0 + 40 * (t) + 8)
-#define O_FULL(t) (tb0 + 40 * (t) + 16)
-#define DRAINED(t) (tb0 + 40 * (t) + 24)
-#define TURN(t) (tb0 + 40 * (t) + 32)
+  const uint32_t tb0 = smem_u32(bars + 2 + 3 * EX_SLOTS);     // per tile: S full, P full, O full, drained
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 10 + 3 * EX_SLOTS);
+#define S_FULL(t) (tb0 + 32 * (t))
+#define P_FULL(t) (tb0 + 32 * (t) + 8)
+#define O_FULL(t) (tb0 + 32 * (t) + 16)
+#define DRAINED(t) (tb0 + 32 * (t) + 24)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0 && lane == 0) {
@@ -394,8 +384,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(S_FULL(t), 1);
-      mbar_init(P_FULL(t), 8);
-      mbar_init(TURN(t), 1);
+      mbar_init(P_FULL(t), 9);                   // the softmax warps, and whoever passes the turn on
       mbar_init(O_FULL(t), 1);
       mbar_init(DRAINED(t), 1);
     }
@@ -569,14 +558,14 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int t = warp - 1;
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0) + 256 * t;
     const uint64_t qd = sw128_desc(smem_u32(smem + S::Q_OFF) + t * (2 * S::SUB));
-    int kv = 0, items = 0, np = 0, turns = 0;
+    int kv = 0, items = 0, np = 0;
     bool ok = true;
+    if (t == 0 && lane == 0) mbar_arrive(P_FULL(0));   // tile A has the first turn
     auto kv_base = [&](int i) { return smem_u32(smem + S::KV_OFF) + (uint32_t)(i % EX_SLOTS) * (2 * S::SUB); };
     auto wait_kv = [&](int i) { return mbar_wait_warp(kv_full0 + 8 * (i % EX_SLOTS), (i / EX_SLOTS) & 1, p.err); };
     // S = Q K^T of fill i, and what else is done once the products issued so far are
-    auto issue_s = [&](int i, bool last) {
+    auto issue_s = [&](int i, uint64_t kd, bool last) {
       if (elect_one()) {
-        const uint64_t kd = sw128_desc(kv_base(i));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {         // 16 head dims a step
           const uint64_t off = (kk >> 2) * (S::SUB >> 4) + 2 * (kk & 3);
@@ -588,9 +577,8 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int i, bool first, bool last) {
+    auto issue_pv = [&](int i, uint64_t vd, bool first, bool last) {
       if (elect_one()) {
-        const uint64_t vd = v_desc(kv_base(i));
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)           // 16 keys a step: 2048 bytes of V, 8 columns of P
           umma_bf16_ta(tb + 128, tb + 8 * kk, vd + 128 * kk, EX_IDESC_PV, (!first || kk > 0) ? 1u : 0u);
@@ -614,23 +602,20 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         ok = wait_kv(kv);
         if (!ok) break;
         tc_fence_after();
-        issue_s(kv, nbk == 1);
+        issue_s(kv, sw128_desc(kv_base(kv)), nbk == 1);
         for (int j = 0; j < nbk; ++j) {
           const int vi = kv + 2 * j + 1;
           const bool last = j + 1 == nbk;
+          const uint64_t vd = v_desc(kv_base(vi)), kd = sw128_desc(kv_base(vi + 1));
           ok = wait_kv(vi) && (last || wait_kv(vi + 1)) && mbar_wait_warp(P_FULL(t), np & 1, p.err);
           if (!ok) break;
           ++np;
-          // the tiles take turns, PV and the next S together: mixed, both would end late and both softmaxes run at once
-          if (both) {
-            ok = mbar_wait_warp(TURN(t), (turns & 1) ^ (t == 0), p.err);
-            if (!ok) break;
-            ++turns;
-          }
           tc_fence_after();
-          issue_pv(vi, j == 0, last);
-          if (!last) issue_s(vi + 1, j + 2 == nbk);
-          if (both && lane == 0) mbar_arrive(TURN(t ^ 1));
+          issue_pv(vi, vd, j == 0, last);
+          if (!last) issue_s(vi + 1, kd, j + 2 == nbk);
+          // the tiles take turns, PV and the next S together: mixed, both would end late and both softmaxes run at
+          // once.  After an item the turn is tile A's again; where there is no tile B it stays there.
+          if (lane == 0) mbar_arrive(P_FULL(both ? t ^ 1 : 0));
         }
       }
       kv += 2 * nbk;
@@ -673,56 +658,69 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
       const int pos[2] = {row_in[0] ? w.q.len - w.q.n + tok0 + tok_r[0] : INT_MAX,
                           row_in[1] ? w.q.len - w.q.n + tok0 + tok_r[1] : INT_MAX};
       // pend: factor that O still has to be scaled by
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, pend[2] = {1.f, 1.f};
+      float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, pend[2] = {1.f, 1.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++ns) {
+        const int lim[2] = {pos[0] - kb * EX_BK, pos[1] - kb * EX_BK};   // keys c <= lim are seen
+        const bool masked = !__all_sync(0xffffffffu, lim[0] >= EX_BK - 1 && lim[1] >= EX_BK - 1);
         ok = mbar_wait_warp(S_FULL(t), ns & 1, p.err);
         if (!ok) break;
         tc_fence_after();
-        const int lim[2] = {pos[0] - kb * EX_BK, pos[1] - kb * EX_BK};   // keys c <= lim are seen
-        const bool masked = !__all_sync(0xffffffffu, lim[0] >= EX_BK - 1 && lim[1] >= EX_BK - 1);
-        // The terms are formed against the reference from the blocks before, while this block's
-        // maximum is found on the way; P replaces S only afterwards.  A reference up to 2^EX_REDO
-        // too low does no harm (P and O have fp32's exponents): it is raised for the next block.
-        // Where it is further off the warp forms the block again.  A unit's first block takes 0, where no key is
-        // masked, and its maximum beforehand where some are (it may be that of none).
+        // The terms are formed against the reference from the blocks before; P replaces S only afterwards.  A
+        // reference that is off by up to 2^64 does no harm (P and O have fp32's exponents); the rows' sums tell
+        // how far it is: beyond EX_MAX_SUM it is raised for the next block, beyond EX_FAR the warp forms the
+        // block again.  A unit's first block takes 0, where no key is masked, and its maximum beforehand where
+        // some are (it may be that of none: -inf).
         uint32_t pk[32];
-        float mx[2], sum[2];
-        if (kb == w.kb0 && masked) {
+        float sum[2];
+        const bool first = kb == w.kb0;
+        if (first && masked) {
+          float mx[2];
           ex_row_max(tS, masked, lim, quad, mx);
           m[0] = mx[0] * p.sl2;
           m[1] = mx[1] * p.sl2;
         }
-        ex_terms(tS, masked, lim, quad, m, p.sl2, pk, mx, sum);
-        // no reference yet (-inf): the terms were formed against 0
-        const bool far[2] = {mx[0] > (m[0] == -INFINITY ? 0.f : m[0]) + EX_REDO ||
-                                 (m[0] == -INFINITY && mx[0] < -EX_REDO && mx[0] > -INFINITY),
-                             mx[1] > (m[1] == -INFINITY ? 0.f : m[1]) + EX_REDO ||
-                                 (m[1] == -INFINITY && mx[1] < -EX_REDO && mx[1] > -INFINITY)};
-        if (__any_sync(0xffffffffu, far[0] || far[1])) {
+        ex_terms(tS, masked, lim, quad, m, p.sl2, pk, sum);
+        const float low = first && !masked ? EX_MIN_SUM : 0.f;
+        auto odd = [&](int e) {
+          return row_in[e] && (!(sum[e] <= EX_MAX_SUM) || sum[e] < low || m[e] == -INFINITY || pend[e] != 1.f);
+        };
+        // what is rare takes one vote, by the thread's own columns: a row's sum is at most four times as much
+        const bool rare = __any_sync(0xffffffffu, odd(0) || odd(1));
+        if (rare) {
+          float mx[2], all[2] = {quad_sum(sum[0]), quad_sum(sum[1])};
+          auto far = [&](int e) {
+            return row_in[e] && lim[e] >= 0 &&
+                   (!(all[e] < EX_FAR) || (((first && !masked) || m[e] == -INFINITY) && all[e] < EX_MIN_SUM));
+          };
+          const bool again[2] = {far(0), far(1)};
+          if (__any_sync(0xffffffffu, again[0] || again[1])) {
+            ex_row_max(tS, masked, lim, quad, mx);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (far[e]) {
-              const float corr = ex2(m[e] - mx[e]);
+            for (int e = 0; e < 2; ++e) {
+              if (!again[e]) continue;
+              mx[e] *= p.sl2;
+              const float corr = first || m[e] == -INFINITY ? 1.f : ex2(m[e] - mx[e]);   // nothing before it otherwise
               l[e] *= corr;
               pend[e] *= corr;
               m[e] = mx[e];
             }
+            ex_terms(tS, masked, lim, quad, m, p.sl2, pk, sum);
+            // ex2_fma takes -inf for a small term: where every score is -inf there is nothing
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (again[e] && m[e] == -INFINITY && sum[e] < 1.f) sum[e] = 0.f;
           }
-          ex_terms(tS, masked, lim, quad, m, p.sl2, pk, mx, sum);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (m[e] == -INFINITY && mx[e] > -INFINITY) m[e] = 0.f;
-        // the product that wrote O last is done: S_j was issued after it
-        if (kb > w.kb0 && __any_sync(0xffffffffu, pend[0] != 1.f || pend[1] != 1.f)) {
+          // the product that wrote O last is done: S_j was issued after it
+          if (!first && __any_sync(0xffffffffu, pend[0] != 1.f || pend[1] != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float o[16];
-            tmem_ld_16x256b(tO + 32 * c, o);
-            tmem_wait_ld16(o);
+            for (int c = 0; c < 4; ++c) {
+              float o[16];
+              tmem_ld_16x256b(tO + 32 * c, o);
+              tmem_wait_ld16(o);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= pend[(k >> 1) & 1];
-            tmem_st_16x256b(tO + 32 * c, o);
+              for (int k = 0; k < 16; ++k) o[k] *= pend[(k >> 1) & 1];
+              tmem_st_16x256b(tO + 32 * c, o);
+            }
           }
         }
         tmem_st_16x128b(tS, pk);
@@ -731,14 +729,20 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(P_FULL(t));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // a NaN that went through ex2_fma is one again (terms end at 2^EX_REDO), a block of -inf adds nothing
-          l[e] += mx[e] == -INFINITY ? 0.f : sum[e] < 0x1p100f ? sum[e] : NAN;
-          pend[e] = 1.f;
-          if (mx[e] > m[e] + EX_RAISE) {
-            pend[e] = ex2(m[e] - mx[e]);
-            l[e] *= pend[e];
-            m[e] = mx[e];
+        for (int e = 0; e < 2; ++e)
+          l[e] += sum[e] < 0x1p100f ? sum[e] : NAN;   // a NaN that went through ex2_fma is one again
+        if (rare) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float all = quad_sum(sum[e]);
+            pend[e] = 1.f;
+            if (m[e] == -INFINITY && all > 0.f) m[e] = 0.f;   // the terms were formed against 0
+            if (all > EX_MAX_SUM && all < 0x1p100f) {         // by a power of two: exact
+              const int up = (__float_as_int(all) >> 23) - 127;
+              pend[e] = __int_as_float((127 - up) << 23);
+              l[e] *= pend[e];
+              m[e] += (float)up;
+            }
           }
         }
       }
@@ -806,7 +810,6 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #undef P_FULL
 #undef O_FULL
 #undef DRAINED
-#undef TURN
 
 // CTA (c, y): rows 32 y .. of the unit whose parts begin in CTA c of the kernel above, a warp per
 // row: o = sum of o_i 2^(m_i - m) / sum of l_i 2^(m_i - m), in the order of the parts.
