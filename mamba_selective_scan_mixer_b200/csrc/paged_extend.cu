@@ -358,11 +358,11 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     const __grid_constant__ CUtensorMap tmV, const ExParams p) {
   using S = ExSmem;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long sh_left, sh_rem;
+  __shared__ long long sh_left, sh_rem, sh_warp[EX_THREADS / 32];
+  __shared__ ExSeq sh_seq;
   __shared__ int sh_pos[4];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::BAR_OFF);
-  long long* sh_sum = reinterpret_cast<long long*>(smem + S::KV_OFF);   // until the first copies
   const uint32_t q_full = smem_u32(bars), q_empty = smem_u32(bars + 1);
   const uint32_t kv_full0 = smem_u32(bars + 2), kv_empty0 = smem_u32(bars + 2 + EX_SLOTS);
   const uint32_t land0 = smem_u32(bars + 2 + 2 * EX_SLOTS);   // a V block with rows to be zeroed has landed
@@ -402,58 +402,47 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int per_t = (p.g.S + EX_THREADS - 1) / EX_THREADS;
     const int s0 = threadIdx.x * per_t, s1 = min(p.g.S, s0 + per_t);
     long long sum = 0;
+    ExSeq q;
     for (int s = s0; s < s1; ++s) {
-      ExSeq q;
       q.load(p, s);
       sum += q.total(p);
     }
-    sh_sum[threadIdx.x] = sum;
-    __syncthreads();
-    if (warp == 0) {                             // inclusive scan, twenty sums a lane
-      long long mine = 0;
-      for (int i = 0; i < EX_THREADS / 32; ++i) mine += sh_sum[lane * (EX_THREADS / 32) + i];
-      long long x = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      long long at = x - mine;
-      for (int i = 0; i < EX_THREADS / 32; ++i) {
-        at += sh_sum[lane * (EX_THREADS / 32) + i];
-        sh_sum[lane * (EX_THREADS / 32) + i] = at;
-      }
+    long long x = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    if (lane == 31) sh_warp[warp] = x;
     __syncthreads();
-    const long long N = sh_sum[EX_THREADS - 1];
+    long long N = 0, mine0 = x - sum;
+    for (int i = 0; i < EX_THREADS / 32; ++i) {
+      if (i < warp) mine0 += sh_warp[i];
+      N += sh_warp[i];
+    }
     long long per = (N + gridDim.x - 1) / gridDim.x;
     if (per < EX_MIN_COST) per = EX_MIN_COST;
     const long long a = min(N, blockIdx.x * per), b = min(N, a + per);
-    const long long mine0 = sh_sum[threadIdx.x] - sum;
     if (b > a && a >= mine0 && a < mine0 + sum) {
       long long rem = a - mine0;
-      ExSeq q;
       for (int s = s0; s < s1; ++s) {
-        q.load(p, s);
-        const long long t = q.total(p);
-        if (rem < t) {
-          const long long head = t / p.g.G;
+        if (s1 - s0 > 1) q.load(p, s);
+        const long long head = q.units ? q.before(p, q.units) : 0, all = head * p.g.G;
+        if (rem < all) {
           const int g = (int)(rem / head);
-          rem -= g * head;
           sh_pos[0] = s;
           sh_pos[1] = g;
-          sh_rem = rem;
+          sh_rem = rem - g * head;
+          sh_seq = q;
           break;
         }
-        rem -= t;
+        rem -= all;
       }
     }
     if (threadIdx.x == 0) sh_left = b - a;
   }
-  fence_async_shared();                          // the sums' memory goes to the copies
   __syncthreads();
   if (warp == 0 && sh_left > 0) {                // the unit: before(lo) <= sh_rem < before(hi), 32 places at a time
-    ExSeq q;
-    q.load(p, sh_pos[0]);
+    const ExSeq q = sh_seq;
     int lo = 0, hi = q.units;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32, at = lo + lane * step;
@@ -477,7 +466,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     w.g = sh_pos[1];
     w.u = sh_pos[2];
     w.at = sh_pos[3];
-    w.q.load(p, w.s);
+    w.q = sh_seq;
   }
 
   // registers go from the first four warps to the softmax warps: 128 * 64 + 512 * 104 = 640 * 96
@@ -704,6 +693,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
               pend[e] *= corr;
               m[e] = mx[e];
             }
+            __syncwarp();                        // the loads are the whole warp's
             ex_terms(tS, masked, lim, quad, m, p.sl2, pk, sum);
             // ex2_fma takes -inf for a small term: where every score is -inf there is nothing
 #pragma unroll
