@@ -693,3 +693,30 @@ def test_scores_that_are_not_finite(J):
                         err = np.abs(o[t, h] - want["o"][t, h])
                         assert (err <= TOL_O * want["spread"][t, h]).all(), (ragged, s, t, h)
                         assert abs(z[t, h] - want["lse"][t, h]) <= 2.0 ** -12 + 2.0 ** -22 * abs(want["lse"][t, h])
+
+
+@pytest.mark.parametrize("lengths,new", [([2000, 1300, 130], [3, 300, 130]), ([128], [128]), ([40, 129, 700], [1, 1, 1])])
+def test_scores_far_from_zero(J, lengths, new):
+    """Heads whose scores all lie near 181, 45, 0, -45 and -181 (times log2 e: 261, 65, ...), within a first block
+    and in later ones, keys of the second half further off by as much again: no reference fits both halves.
+
+    Tolerance: the large product is exact, so the scores' error is that of adding 127 small products to at most
+    2 * 2048, half a step of 2^-11 each: 127 * 2^-12 / sqrt(128) < 2^-8.4, on a term and on the sum, 2^-7.4 beside
+    TOL_O; of the lse once, beside fp32's rounding of it."""
+    G, H, P = 2, 16, 64
+    rng = np.random.default_rng(81)
+    k, v, table = _cache(rng, lengths, G, P)
+    q = _q(sum(new), H, G, 81)
+    q[:, :, 0] = torch.tensor([8.0, 2.0, 0.0, -2.0, -8.0, 8.0, -8.0, 0.25] * 2, device="cuda", dtype=BF)
+    for s, n in enumerate(lengths):
+        for pos in range(n):
+            k[table[s, pos // P], :, pos % P, 0] = 256.0 if pos < n // 2 else 512.0
+    start = np.concatenate([[0], np.cumsum(new)])
+    args = (k.cuda(), v.cuda(), _i32(table), _i32(lengths))
+    want = op.attention(to_np(q), to_np(k), to_np(v), table, np.array(lengths), start)
+    last = start[1:] - 1
+    for got, lse, rows in (J.paged_extend(q, *args, _i32(start), want_lse=True) + (np.arange(sum(new)),),
+                           J.paged_decode(q[torch.tensor(last, device="cuda")], *args, want_lse=True) + (last,)):
+        err = np.abs(to_np(got) - want["o"][rows])
+        assert (err <= (TOL_O + 2.0 ** -7.4) * want["spread"][rows]).all()
+        assert (np.abs(to_np(lse) - want["lse"][rows]) <= 2.0 ** -8.4 + 2.0 ** -20 * np.abs(want["lse"][rows])).all()
