@@ -322,9 +322,8 @@ def _plain_compact(s):
     remap = torch.where(mover, holes[rank], torch.where(live, i, -1))
     held = torch.arange(table.shape[1], device=DEV) < -(-s["lengths"][:, None] // P)
     table.copy_(torch.where(held, remap[table.clamp(min=0).long()].to(torch.int32), table))
-    # the page that each one takes its rows from: the mover whose hole it is, or itself
-    source = i.clone().index_put_((torch.where(mover, remap, i),), i)
-    source = torch.where(hole, source, i)
+    # the page that each one takes its rows from: the mover whose hole it is, or itself (the others write past the end)
+    source = torch.arange(N + 1, device=DEV).index_put_((torch.where(mover, remap, N),), i)[:N]
     data.copy_(data[:, source])
     moved = torch.zeros_like(refs).index_add_(0, remap.clamp(min=0), torch.where(live, refs, 0))
     refs.copy_(moved)
