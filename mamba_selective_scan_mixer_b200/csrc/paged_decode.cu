@@ -87,6 +87,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// slot 0 of the join has been read by warp 0 (which only arrives) before warps 2 and 3 write the next item's
+__device__ __forceinline__ void join_read_arrive() { asm volatile("bar.arrive 2, 96;" ::: "memory"); }
+__device__ __forceinline__ void join_read_wait() { asm volatile("bar.sync 2, 96;" ::: "memory"); }
 
 // One stretch of blocks [kb0, kb1) of unit (s, g); every warp walks the same items.
 struct DpWalk {
@@ -271,6 +274,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
       }
       const int qs = items & 1;
       mbar_wait_warp(qfull0 + 8 * qs, (items >> 1) & 1, p.err);
+      __syncwarp();
+      if (warp == 0 && !first_item) join_read_arrive();
       // B fragments of Q^T (k = head dims, n = head gq of each tile; heads past rep are zero)
       uint32_t qb[NT][8][2];
 #pragma unroll
@@ -417,7 +422,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_consta
             }
           }
       };
-      if (warp >= 2) put(warp - 2);
+      if (warp >= 2) {
+        if (!first_item) join_read_wait();
+        put(warp - 2);
+      }
       consumer_sync();
       if (warp < 2) add(warp);
       consumer_sync();

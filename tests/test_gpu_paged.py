@@ -720,3 +720,24 @@ def test_scores_far_from_zero(J, lengths, new):
         err = np.abs(to_np(got) - want["o"][rows])
         assert (err <= (TOL_O + 2.0 ** -7.4) * want["spread"][rows]).all()
         assert (np.abs(to_np(lse) - want["lse"][rows]) <= 2.0 ** -8.4 + 2.0 ** -20 * np.abs(want["lse"][rows])).all()
+
+
+# ------------------------------------------------ many short items in one CTA
+
+@pytest.mark.parametrize("H", [64, 128])               # one and two tiles of eight heads
+@pytest.mark.parametrize("most", [16, 32])             # half the warps, or three quarters, have no position to look at
+def test_decode_many_short_sequences(J, H, most):
+    """700 sequences of 0 to 32 tokens, 8 KV heads: a CTA walks some 19 items, each joined through the same shared
+    memory as the one before while the faster warps are at the next.  Every repeat gives the same bits."""
+    G, P, S = 8, 16, 700
+    rng = np.random.default_rng(H + most)
+    lengths = rng.integers(0, most + 1, S).tolist()
+    k, v, table = _cache(rng, lengths, G, P)
+    q = _q(S, H, G, H)
+    args = (q, k.cuda(), v.cuda(), _i32(table), _i32(lengths))
+    got, lse = J.paged_decode(*args, want_lse=True)
+    want = op.attention(to_np(q), to_np(k), to_np(v), table, np.array(lengths), np.arange(S + 1))
+    _check(got, lse, want)
+    for _ in range(50):
+        again, z = J.paged_decode(*args, want_lse=True)
+        assert torch.equal(again, got) and torch.equal(z, lse)
