@@ -247,15 +247,17 @@ constexpr int EX_FMA_EVERY = 4;    // of the pairs of terms, one in so many goes
 constexpr float EXC0 = 0.99999926144f, EXC1 = 0.69312181475f, EXC2 = 0.24024744849f, EXC3 = 0.05591786025f,
                 EXC4 = 0.00957010107f;
 
-// 2^x for both halves on the FMA pipe, x in [-126, 126] (lower ones count as -126): the nearest
-// integer n through the mantissa of x + 1.5 2^23, a degree-4 polynomial for 2^f with f = x - n in
-// [-1/2, 1/2] (fitted for the least largest relative error, 2.6e-6; P keeps 2^-9), and n added to its
-// exponent; a NaN comes out as one or above 2^126.  Takes some of the terms because ex2 alone runs at
-// 16 a cycle and SM: 128 x 256 terms take the 2048 cycles that their four products take.
+// 2^x for both halves on the FMA pipe, x taken into [-126, 127]: the nearest integer n through the
+// mantissa of x + 1.5 2^23, a degree-4 polynomial for 2^f with f = x - n in [-1/2, 1/2] (fitted for
+// the least largest relative error, 2.6e-6; P keeps 2^-9), and n added to its exponent.  Below the range the
+// result, some 2^-126, is as good as none; above it and for a NaN it is at least 2^126, which the row's sum
+// shows.  Without the upper limit the exponent would run into the sign and a far key vanish.  Takes some of the
+// terms because ex2 alone runs at 16 a cycle and SM: 128 x 256 terms take the 2048 cycles that their
+// four products take.
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
   const float big = 12582912.f;
-  x.x = nan_max(x.x, -126.f);
-  x.y = nan_max(x.y, -126.f);
+  x.x = fminf(nan_max(x.x, -126.f), 127.f);      // a NaN becomes 127
+  x.y = fminf(nan_max(x.y, -126.f), 127.f);
   const float2 one = make_float2(1.f, 1.f);
   const float2 t = ffma2(x, one, make_float2(big, big));
   const float2 n = ffma2(t, one, make_float2(-big, -big));

@@ -741,3 +741,32 @@ def test_decode_many_short_sequences(J, H, most):
     for _ in range(50):
         again, z = J.paged_decode(*args, want_lse=True)
         assert torch.equal(again, got) and torch.equal(z, lse)
+
+
+# --------------------------------------------------- one key far from the others
+
+@pytest.mark.parametrize("nats", [134, 198, 282])
+@pytest.mark.parametrize("cached,at", [(200, 0), (400, 256)])
+def test_extend_one_far_key(J, nats, cached, at):
+    """One key of a sequence lies 95, 140 or 200 nats above the others for every row, in turn at each of the
+    128 columns of a first unmasked block or of a later one: it has all the weight, in units that one CTA takes
+    and in ones that are cut into parts, as in the path of single tokens.
+
+    Tolerance: as in test_scores_far_from_zero; the large product, at most 8 * 282 < 4096, is exact."""
+    G, H, P, n = 2, 8, 64, 4
+    S = 128
+    lengths = [cached + n] * S
+    rng = np.random.default_rng(nats + at)
+    k, v, table = _cache(rng, lengths, G, P)
+    q = _q(S * n, H, G, 91)
+    q[:, :, 0] = 8.0
+    for s in range(S):
+        for pos in range(lengths[s]):
+            k[table[s, pos // P], :, pos % P, 0] = float(nats) if pos == at + s else 0.0
+    start = np.arange(S + 1) * n
+    args = (k.cuda(), v.cuda(), _i32(table), _i32(lengths))
+    got, lse = J.paged_extend(q, *args, _i32(start), want_lse=True)
+    want = op.attention(to_np(q), to_np(k), to_np(v), table, np.array(lengths), start)
+    err = np.abs(to_np(got) - want["o"])
+    assert (err <= (TOL_O + 2.0 ** -7.4) * want["spread"]).all()
+    assert (np.abs(to_np(lse) - want["lse"]) <= 2.0 ** -8.4 + 2.0 ** -20 * np.abs(want["lse"])).all()
