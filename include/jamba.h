@@ -702,8 +702,9 @@ jamba_status jamba_paged_decode(const jamba_pages_config* cfg, int n_heads, cons
  * A token before position 0 gets o = 0 and lse = -inf; rows of q past
  * q_start[max_seqs] are left out.  A key that is not finite reaches the tokens that
  * see it, a value that is not finite any new token of its sequence (it enters the
- * products of earlier ones with weight 0), neither another sequence.  At most 128
- * query heads per KV head.
+ * products of earlier ones with weight 0), neither another sequence.  Finite values
+ * up to 2^80 in size and scores up to 2^30 (in size, after the scale) are safe: sums
+ * of larger ones may leave fp32's range.  At most 128 query heads per KV head.
  * Errors as jamba_paged_decode. */
 jamba_status jamba_paged_extend(const jamba_pages_config* cfg, int n_heads, const void* q, int ld_q, int tokens,
                                 const int32_t* q_start, const void* k_pages, const void* v_pages,

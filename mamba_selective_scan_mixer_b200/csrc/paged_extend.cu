@@ -167,8 +167,10 @@ struct ExWalk {
 
 // a row's terms in one block add up to more than this: the reference is raised, to even the exponents
 constexpr float EX_MAX_SUM = 0x1p16f;
-// ... to more than this, or to less than EX_MIN_SUM in a first block: the block is formed again
-constexpr float EX_FAR = 0x1p64f, EX_MIN_SUM = 0x1p-64f;
+// ... to more than this, or to less than EX_MIN_SUM in a first block: the block is formed again.  So |O| stays below
+// 2^40 max |v| (2^23 blocks of up to EX_MAX_SUM, one of up to EX_FAR), and of a row's terms the largest above 2^-40:
+// values from 2^-80 to 2^80 in size keep fp32's precision in the products.
+constexpr float EX_FAR = 0x1p32f, EX_MIN_SUM = 0x1p-32f;
 
 // Softmax warps hold 16 rows of a tile each: in tcgen05.ld / st .16x256b and .16x128b a row's columns
 // lie over the four lanes of a quad (lane i: rows i / 4 and i / 4 + 8; of each 8 columns of 32
@@ -657,8 +659,7 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         if (!ok) break;
         tc_fence_after();
         // The terms are formed against the reference from the blocks before; P replaces S only afterwards.  A
-        // reference that is off by up to 2^64 does no harm (P and O have fp32's exponents); the rows' sums tell
-        // how far it is: beyond EX_MAX_SUM it is raised for the next block, beyond EX_FAR the warp forms the
+        // reference that is off by up to 2^32 does no harm (see EX_FAR); the rows' sums tell how far it is: beyond EX_MAX_SUM it is raised for the next block, beyond EX_FAR the warp forms the
         // block again.  A unit's first block takes 0, where no key is masked, and its maximum beforehand where
         // some are (it may be that of none: -inf).
         uint32_t pk[32];

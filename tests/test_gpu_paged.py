@@ -770,3 +770,30 @@ def test_extend_one_far_key(J, nats, cached, at):
     err = np.abs(to_np(got) - want["o"])
     assert (err <= (TOL_O + 2.0 ** -7.4) * want["spread"]).all()
     assert (np.abs(to_np(lse) - want["lse"]) <= 2.0 ** -8.4 + 2.0 ** -20 * np.abs(want["lse"])).all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_extend_far_scores_with_values_of_any_size(J, sign):
+    """Scores 37 nats above the reference with values around 2^80, and 37 nats below it with values around 2^-80:
+    neither the terms nor their products leave fp32's range.
+
+    Tolerance: as in test_scores_far_from_zero; the large product, 8 * 52, is exact and below 512, so the scores'
+    error is below 127 * 2^-15 / sqrt(128) < 2^-8.4 all the more."""
+    G, H, P, n = 2, 8, 64, 4
+    lengths = [300, 1300, 90, 2000]
+    S = len(lengths)
+    rng = np.random.default_rng(95)
+    k, v, table = _cache(rng, lengths, G, P)
+    v = v * 2.0 ** (80 * sign)
+    q = _q(S * n, H, G, 95)
+    q[:, :, 0] = 8.0
+    for s in range(S):
+        for pos in range(lengths[s]):
+            k[table[s, pos // P], :, pos % P, 0] = 52.0 * sign
+    start = np.arange(S + 1) * n
+    args = (k.cuda(), v.cuda(), _i32(table), _i32(lengths))
+    got, lse = J.paged_extend(q, *args, _i32(start), want_lse=True)
+    want = op.attention(to_np(q), to_np(k), to_np(v), table, np.array(lengths), start)
+    err = np.abs(to_np(got) - want["o"])
+    assert (err <= (TOL_O + 2.0 ** -7.4) * want["spread"]).all()
+    assert (np.abs(to_np(lse) - want["lse"]) <= 2.0 ** -8.4 + 2.0 ** -20 * np.abs(want["lse"])).all()
