@@ -650,6 +650,18 @@ jamba_status jamba_pages_grow(const jamba_pages_config* cfg, const int32_t* add,
                               int32_t* table, int32_t* lengths, int32_t* granted, void* ws, size_t ws_bytes,
                               jamba_stream_t stream);
 
+/* The lengths to call jamba_paged_append, the attention and the layer with when some
+ * slots take no part: out[s] = lengths[s] where active[s] > 0, 0 elsewhere.  A slot of
+ * length 0 is not written and attends to nothing, whatever it holds.  With one token
+ * for every slot (no q_start) each slot of a length is written at its last position: a slot
+ * that brings no token, or that jamba_pages_grow refused, would lose its last key and value, and
+ * so would every slot that shares the page; the same holds of a refused slot's rows in a
+ * ragged batch.  active = granted * add of that call leaves both out.
+ *   active, lengths, out [max_seqs] int32 (out may be lengths)
+ * Errors: INVALID_ARG, CUDA. */
+jamba_status jamba_pages_active(int max_seqs, const int32_t* active, const int32_t* lengths, int32_t* out,
+                                jamba_stream_t stream);
+
 /* Moves the live pages to the front of the pool: with n live pages, those
  * numbered n and up move, in ascending order, into the free pages below n, in
  * ascending order; rows of all planes, counts and table entries follow.
@@ -666,7 +678,7 @@ jamba_status jamba_pages_compact(const jamba_pages_config* cfg, void* data, int3
  *         (a multiple of 8, at least n_kv_heads * head_dim)
  *   q_start [max_seqs + 1] int32, ascending, q_start[max_seqs] = tokens; or
  *         NULL with tokens = max_seqs: one token for every sequence, the
- *         empty ones (length 0) left out
+ *         empty ones (length 0) left out (see jamba_pages_active)
  *   k_pages, v_pages: their planes, [num_pages, n_kv_heads, page_size, head_dim]
  * cfg->planes is not read.  Tokens that no sequence counts, or that would stand
  * before position 0, are not written.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
@@ -713,7 +725,8 @@ jamba_status jamba_paged_extend(const jamba_pages_config* cfg, int n_heads, cons
 
 /* The attention layer over the paged cache: fused q|k|v projection, append,
  * attention, out_proj (+ residual).  pages->n_kv_heads and head_dim are the
- * layer's; lengths already count the new tokens (jamba_pages_grow).
+ * layer's; lengths already count the new tokens (jamba_pages_grow) and are 0 for
+ * slots that take no part (jamba_pages_active).
  * prefill: x, residual, out [tokens, d_model], ragged as in jamba_paged_extend;
  *   a row that no sequence counts attends to nothing (its output is the residual, or 0).
  * step: one token for every slot, x, residual, out [max_seqs, d_model]; slots of length 0

@@ -115,6 +115,7 @@ SIGNATURES = {
     "jamba_pages_workspace_size": [P, ctypes.POINTER(SZ)],
     "jamba_pages_fork": [P, P, P, P, P, P, SZ, P],
     "jamba_pages_grow": [P, P, P, P, P, P, P, P, SZ, P],
+    "jamba_pages_active": [I, P, P, P, P],
     "jamba_pages_compact": [P, P, P, P, P, P, P, SZ, P],
     "jamba_paged_append": [P, P, P, I, I, P, P, P, P, P, P],
     "jamba_paged_decode_workspace_size": [P, I, ctypes.POINTER(SZ)],

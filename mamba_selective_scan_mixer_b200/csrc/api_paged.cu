@@ -12,6 +12,7 @@ using namespace jb;
 namespace {
 
 constexpr int DECODE_MAX_REP = 16;    // query heads per KV head of the one-token kernel
+constexpr int MAX_SLOTS = 1 << 20;
 constexpr int EXTEND_MAX_REP = 128;   // ... of the ragged kernel: one token's heads fill its rows of a tile
 
 jamba_status geom(const jamba_pages_config* c, PageGeom* g) {
@@ -30,7 +31,7 @@ jamba_status geom(const jamba_pages_config* c, PageGeom* g) {
   if (c->n_kv_heads > 1024) return fail(JAMBA_ERR_UNSUPPORTED, "pages: at most 1024 KV heads");
   if (((long long)c->num_pages * c->n_kv_heads << shift) > INT_MAX)
     return fail(JAMBA_ERR_UNSUPPORTED, "pages: more than 2^31 - 1 rows in a plane");
-  if (c->max_seqs > (1 << 20)) return fail(JAMBA_ERR_UNSUPPORTED, "pages: at most 2^20 slots");
+  if (c->max_seqs > MAX_SLOTS) return fail(JAMBA_ERR_UNSUPPORTED, "pages: at most 2^20 slots");
   *g = {c->num_pages, c->n_kv_heads, shift, c->planes, c->max_seqs, c->max_pages, c->ld_table};
   return JAMBA_OK;
 }
@@ -172,6 +173,17 @@ jamba_status jamba_pages_grow(const jamba_pages_config* cfg, const int32_t* add,
   JB_TRY(check_upkeep(g, refs, table, lengths, ws, ws_bytes, "pages grow"));
   JB_TRY(ready());
   return pages_grow(g, add, data, refs, table, lengths, granted, ws, cs(stream));
+}
+
+jamba_status jamba_pages_active(int max_seqs, const int32_t* active, const int32_t* lengths, int32_t* out,
+                                jamba_stream_t stream) {
+  JB_RANGE("jamba_pages_active");
+  if (max_seqs <= 0 || max_seqs > MAX_SLOTS)
+    return fail(JAMBA_ERR_INVALID_ARG, "pages active: max_seqs must be 1 .. 2^20");
+  JB_TRY(check_int(active, "active"));
+  JB_TRY(check_int(lengths, "lengths"));
+  JB_TRY(check_int(out, "out"));
+  return pages_active(max_seqs, active, lengths, out, cs(stream));
 }
 
 jamba_status jamba_pages_compact(const jamba_pages_config* cfg, void* data, int32_t* refs, int32_t* table,

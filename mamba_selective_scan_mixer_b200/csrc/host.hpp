@@ -239,6 +239,7 @@ jamba_status pages_fork(const PageGeom& g, const int* parent, int* refs, int* ta
                         cudaStream_t s);
 jamba_status pages_grow(const PageGeom& g, const int* add, void* data, int* refs, int* table, int* lengths,
                         int* granted, void* ws, cudaStream_t s);
+jamba_status pages_active(int S, const int* active, const int* lengths, int* out, cudaStream_t s);
 jamba_status pages_compact(const PageGeom& g, void* data, int* refs, int* table, const int* lengths, int* remap,
                            void* ws, cudaStream_t s);
 jamba_status paged_append(const PageGeom& g, const void* k, const void* v, int ld, int tokens, const int* q_start,

@@ -261,6 +261,15 @@ pages_grow_apply_kernel(PageGeom g, bf16* __restrict__ data, int* refs, int* __r
   }
 }
 
+// out[s] = lengths[s] of the slots that take part, 0 of the others; a thread per slot, bound by the launch.
+__global__ void __launch_bounds__(256)
+pages_active_kernel(int S, const int* active, const int* lengths, int* out) {
+  griddep_wait();
+  griddep_launch();
+  const int s = blockIdx.x * 256 + threadIdx.x;
+  if (s < S) out[s] = active[s] > 0 ? lengths[s] : 0;
+}
+
 // ---------------------------------------------------------------- compact
 
 // One CTA: remap, and the pairs (mover -> hole).  counts[0] = pages that move.
@@ -439,6 +448,11 @@ jamba_status pages_grow(const PageGeom& g, const int* add, void* data, int* refs
   JB_CUDA(launch_pdl(pages_grow_apply_kernel, dim3(grid), dim3(256), 0, s, g, reinterpret_cast<bf16*>(data), refs,
                      table, lengths, granted, (const GrowRecord*)w.rec, (const int*)w.free_list,
                      (const int*)w.copiers, (const int*)w.counts));
+  return JAMBA_OK;
+}
+
+jamba_status pages_active(int S, const int* active, const int* lengths, int* out, cudaStream_t s) {
+  JB_CUDA(launch_pdl(pages_active_kernel, dim3((S + 255) / 256), dim3(256), 0, s, S, active, lengths, out));
   return JAMBA_OK;
 }
 

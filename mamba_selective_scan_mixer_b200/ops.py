@@ -458,11 +458,12 @@ class Attention:
                                     _stream(stream)))
         return out
 
-    def _paged(self, x, cache, layer, tokens, q_start, residual, out, stream):
+    def _paged(self, x, cache, layer, tokens, q_start, residual, out, active, stream):
         if self.shape.n_kv_heads != cache.data.shape[2]:
             raise ValueError("the cache holds %d KV heads" % cache.data.shape[2])
         named = (("x", x), ("w_o", self.w_o)) + tuple(
-            (n, t) for n, t in (("residual", residual), ("out", out), ("q_start", q_start)) if t is not None)
+            (n, t) for n, t in (("residual", residual), ("out", out), ("q_start", q_start), ("active", active))
+            if t is not None)
         index = paged._same_device(cache.data, named)
         for t, name in ((x, "x"), (residual, "residual"), (out, "out")):
             _contig(t, name)
@@ -478,6 +479,7 @@ class Attention:
             out = torch.empty_like(x) if out is None else out
             if tokens == 0:
                 return out
+            lengths = cache.lengths if active is None else cache.active_lengths(active)
             n = ctypes.c_size_t()
             if q_start is None:
                 check(L.jamba_attn_paged_step_workspace_size(a, cfg, ctypes.byref(n)))
@@ -486,28 +488,32 @@ class Attention:
             ws = torch.empty(n.value, dtype=torch.uint8, device=x.device)
             if q_start is None:
                 check(L.jamba_attn_paged_step(a, w, cfg, _p(x), _p(residual), _p(out), _p(k), _p(v), _p(cache.table),
-                                              _p(cache.lengths), _p(ws), ws.numel(), st))
+                                              _p(lengths), _p(ws), ws.numel(), st))
             else:
                 check(L.jamba_attn_paged_prefill(a, w, cfg, _p(x), _p(residual), _p(out), tokens, _p(q_start), _p(k),
-                                                 _p(v), _p(cache.table), _p(cache.lengths), _p(ws), ws.numel(), st))
+                                                 _p(v), _p(cache.table), _p(lengths), _p(ws), ws.numel(), st))
             return out
 
         return paged._run(index, stream, body, out)
 
-    def paged_prefill(self, x, q_start, cache, layer=0, residual=None, out=None, stream=None):
+    def paged_prefill(self, x, q_start, cache, layer=0, residual=None, out=None, stream=None, active=None):
         """x [tokens, d_model], the new tokens of all slots of a PagedKVCache one
         after another (rows q_start[s] .. q_start[s+1] - 1 are slot s's; the
         cache's lengths count them, see its grow): appends their keys and values to
-        the layer's pages and attends causally over everything each slot holds."""
+        the layer's pages and attends causally over everything each slot holds.  With active
+        [max_seqs] int32, rows of slots where it is 0 or below (grow refused them) write nothing and
+        attend to nothing; without, they would replace the slot's last keys and values."""
         if x.dim() != 2:
             raise ValueError("x must be [tokens, d_model]")
         paged._ints(q_start, "q_start", (cache.table.shape[0] + 1,))
-        return self._paged(x, cache, layer, x.shape[0], q_start, residual, out, stream)
+        return self._paged(x, cache, layer, x.shape[0], q_start, residual, out, active, stream)
 
-    def paged_step(self, x, cache, layer=0, residual=None, out=None, stream=None):
-        """x [max_seqs, d_model], one new token for every slot (empty slots are
-        left out; the cache's lengths count the new tokens)."""
-        return self._paged(x, cache, layer, cache.table.shape[0], None, residual, out, stream)
+    def paged_step(self, x, cache, layer=0, residual=None, out=None, stream=None, active=None):
+        """x [max_seqs, d_model], one new token for every slot (the cache's lengths count
+        them).  Empty slots are left out, and with active [max_seqs] int32 those where it is 0
+        or below: pass granted * add of the grow before it unless every slot that holds anything
+        has grown, for a slot's token is written at its last position."""
+        return self._paged(x, cache, layer, cache.table.shape[0], None, residual, out, active, stream)
 
 
 def layer_pair(mixer, moe, x, g1, g2, eps=1e-6, stream=None):

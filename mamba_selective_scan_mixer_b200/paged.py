@@ -180,6 +180,26 @@ def pages_grow(add, data, refs, table, lengths, stream=None):
     return _run(index, stream, body)
 
 
+def pages_active(active, lengths, stream=None):
+    """lengths with 0 in place of the slots that take no part in a call (active [max_seqs]
+    int32, 0 or below): what paged_append and the attention take then.  A slot that brings no
+    token, or that grow refused, must be left out of a call with one token per slot, and a refused one's
+    rows out of a ragged call, or its last keys and values are overwritten, for every holder of the
+    page; active = granted * add leaves both out."""
+    index = _same_device(lengths, (("active", active),))
+    if lengths.dim() != 1:
+        raise ValueError("lengths must have shape [max_seqs]")
+    _ints(lengths, "lengths", lengths.shape)
+    _ints(active, "active", lengths.shape)
+
+    def body(st):
+        out = torch.empty_like(lengths)
+        check(lib().jamba_pages_active(lengths.shape[0], _p(active), _p(lengths), _p(out), st))
+        return out
+
+    return _run(index, stream, body)
+
+
 def pages_compact(data, refs, table, lengths, stream=None):
     """Moves the live pages to the front of the pool.  Returns remap [num_pages]
     int32: each live page's new number, -1 for free pages."""
@@ -198,7 +218,8 @@ def pages_compact(data, refs, table, lengths, stream=None):
 def paged_append(k, v, k_pages, v_pages, table, lengths, q_start=None, stream=None):
     """Keys and values k, v [tokens, n_kv_heads, 128] of the sequences' last
     tokens into their pages: sequence s has rows q_start[s] .. q_start[s+1] - 1
-    (q_start [max_seqs + 1] int32), or one row each without q_start."""
+    (q_start [max_seqs + 1] int32), or one row each without q_start (slots of length 0
+    left out; see pages_active)."""
     named = (("k", k), ("v", v), ("v_pages", v_pages), ("table", table), ("lengths", lengths))
     index = _same_device(k_pages, named if q_start is None else named + (("q_start", q_start),))
     N, G, P, _ = _planes(k_pages, v_pages)
@@ -279,7 +300,9 @@ class PagedKVCache:
 
     A turn of a server: fork / free the slots that change, grow by the tokens
     each slot brings (granted says which could), then Attention.paged_prefill or
-    paged_step of every layer, which write the new keys and values and attend.
+    paged_step of every layer, which write the new keys and values and attend.  Slots that
+    could not grow, and in paged_step those that bring no token, are left out with
+    active=granted * add (see pages_active).
     """
 
     def __init__(self, layers, n_kv_heads, num_pages, max_seqs, max_len, page_size=64, device="cuda"):
@@ -317,6 +340,10 @@ class PagedKVCache:
     def grow(self, add, stream=None):
         """See pages_grow."""
         return pages_grow(add, self.data, self.refs, self.table, self.lengths, stream=stream)
+
+    def active_lengths(self, active, stream=None):
+        """See pages_active."""
+        return pages_active(active, self.lengths, stream=stream)
 
     def compact(self, stream=None):
         """See pages_compact."""

@@ -797,3 +797,78 @@ def test_extend_far_scores_with_values_of_any_size(J, sign):
     err = np.abs(to_np(got) - want["o"])
     assert (err <= (TOL_O + 2.0 ** -7.4) * want["spread"]).all()
     assert (np.abs(to_np(lse) - want["lse"]) <= 2.0 ** -8.4 + 2.0 ** -20 * np.abs(want["lse"])).all()
+
+
+# ------------------------------------------------------ slots that take no part
+
+def _full_pool(J, seed):
+    """Two slots that share the pages of a prompt of 40, a third of 16 of its own: no page is left, so neither of
+    the first two can take a copy of the shared last page."""
+    att, p = _layer(J)
+    cache = J.PagedKVCache(layers=1, n_kv_heads=2, num_pages=4, max_seqs=4, max_len=64, page_size=16)
+    x = attn_input(SH, 1, 64, seed=seed)[0].cuda()
+    assert cache.grow(_i32([40, 0, 8, 0])).tolist() == [1] * 4
+    att.paged_prefill(x[:48], _i32([0, 40, 40, 48, 48]), cache)
+    cache.fork(_i32([0, 0, 2, 3]))
+    return att, p, cache, x
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("captured", [False, True])
+def test_refused_slots_and_slots_without_a_token_keep_their_rows(J, ragged, captured):
+    """A pool that runs dry under two forks, with a slot that grows, an empty one, and then with no slot growing: with
+    active = granted * add no row changes but the new one's, eagerly and in a graph; the slots left out get the residual."""
+    att, p, cache, x = _full_pool(J, 97)
+    add = _i32([1, 1, 1, 0])
+    new = x[48:52].contiguous()
+    q_start = _i32([0, 1, 2, 3, 4])
+
+    def turn():
+        granted = cache.grow(add)
+        args = dict(cache=cache, residual=new, active=granted * add)
+        return granted, att.paged_prefill(new, q_start, **args) if ragged else att.paged_step(new, **args)
+
+    before = cache.data.clone()
+    J.device_status()
+    graph = None
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            granted, out = turn()
+        graph.replay()
+    else:
+        granted, out = turn()
+    assert granted.tolist() == [0, 0, 1, 1] and cache.lengths.tolist() == [40, 40, 9, 0]
+    changed = (cache.data != before).any(-1).nonzero().tolist()
+    page = int(cache.table[2, 0])
+    assert sorted(changed) == [[plane, page, g, 8] for plane in range(2) for g in range(2)]
+    assert torch.equal(out[[0, 1, 3]], new[[0, 1, 3]]) and not torch.equal(out[2], new[2])
+    want = oatt.attention_prefill(p, to_np(torch.cat([x[40:48], x[50:51]])[None]), SH)["out"][0, -1]
+    assert rel_l2(to_np(out[2]), want + to_np(new[2])) < TOL_BF16
+    add.zero_()                                          # live slots without a token
+    before = cache.data.clone()
+    if captured:
+        graph.replay()
+    else:
+        granted, out = turn()
+    assert granted.tolist() == [1] * 4 and torch.equal(cache.data, before) and torch.equal(out, new)
+
+
+def test_active_lengths(J):
+    n = 1000
+    lengths, active = torch.arange(n, dtype=torch.int32, device="cuda"), _i32(np.arange(n) % 4 - 1)
+    want = torch.where(active > 0, lengths, 0)
+    assert torch.equal(J.pages_active(active, lengths), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = J.pages_active(active, lengths, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    for a, ln in ((active[:5], lengths), (active.long(), lengths), (active[::2], lengths[::2]), (active.cpu(), lengths),
+                  (active[None], lengths[None])):
+        with pytest.raises(ValueError):
+            J.pages_active(a, ln)
+    att, _, cache, x = _full_pool(J, 98)
+    with pytest.raises(ValueError):
+        att.paged_step(x[:4].contiguous(), cache, active=torch.ones(4, dtype=torch.bool, device="cuda"))

@@ -149,3 +149,9 @@ def test_binding_refuses_host_tensors():
                  lambda: J.pages_compact(pages[None], refs, table, lengths)):
         with pytest.raises(ValueError, match="CUDA tensors only"):
             call()
+
+
+def test_active_lengths_refuse_before_a_launch(lib):
+    p, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 2)
+    for args in ((0, p, p, p), ((1 << 20) + 1, p, p, p), (4, None, p, p), (4, p, odd, p), (4, p, p, None)):
+        assert lib.jamba_pages_active(*args, None) == 1, args
