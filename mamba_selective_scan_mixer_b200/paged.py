@@ -325,15 +325,23 @@ class PagedKVCache:
         pages_fork(parent, self.refs, self.table, self.lengths, self.page_size, stream=stream)
 
     def free(self, slots, stream=None):
-        """Frees slots (an index or a list of them)."""
-        parent = list(range(self.table.shape[0]))
-        for s in [slots] if isinstance(slots, int) else slots:
-            if not 0 <= s < len(parent):
-                raise ValueError("slot %d is outside 0 .. %d" % (s, len(parent) - 1))
-            parent[s] = -1
+        """Frees slots (an index or a list of them).  The slots are host values: in a captured
+        graph every replay frees the same ones; fork with -1 frees by device values."""
+        S, device = self.table.shape[0], self.table.device
+        slots = [slots] if isinstance(slots, int) else list(slots)
+        for s in slots:
+            if not 0 <= s < S:
+                raise ValueError("slot %d is outside 0 .. %d" % (s, S - 1))
 
         def body(_):
-            self.fork(torch.tensor(parent, dtype=torch.int32, device=self.table.device))
+            if torch.cuda.is_current_stream_capturing():   # no copy of pageable memory there: a fill for each
+                parent = torch.arange(S, dtype=torch.int32, device=device)
+                for s in slots:
+                    parent[s].fill_(-1)
+            else:
+                gone = set(slots)
+                parent = torch.tensor([-1 if s in gone else s for s in range(S)], dtype=torch.int32, device=device)
+            self.fork(parent)
 
         _run(self.table.get_device(), stream, body)
 

@@ -872,3 +872,22 @@ def test_active_lengths(J):
     att, _, cache, x = _full_pool(J, 98)
     with pytest.raises(ValueError):
         att.paged_step(x[:4].contiguous(), cache, active=torch.ones(4, dtype=torch.bool, device="cuda"))
+
+
+def test_free_in_a_graph(J):
+    """free captured with grow: each replay frees the same slots and gives their pages to the next prompts."""
+    cache = J.PagedKVCache(layers=1, n_kv_heads=2, num_pages=10, max_seqs=3, max_len=64, page_size=16)
+    add = _i32([20, 30, 5])
+    cache.grow(add)
+    cache.free([0, 2])                                    # eagerly
+    assert cache.lengths.tolist() == [0, 30, 0] and int((cache.refs > 0).sum()) == 2
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        cache.free(2)
+        cache.free([0, 1])
+        granted = cache.grow(add)
+    for _ in range(3):
+        graph.replay()
+        assert granted.tolist() == [1, 1, 1] and cache.lengths.tolist() == [20, 30, 5]
+        assert int((cache.refs > 0).sum()) == 5 and int(cache.refs.sum()) == 5
