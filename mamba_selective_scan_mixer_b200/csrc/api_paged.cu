@@ -74,7 +74,26 @@ jamba_status check_heads(const PageGeom& g, int n_heads, int tokens, int max_rep
   return JAMBA_OK;
 }
 
-jamba_status check_attn_args(int n_heads, const void* q, int ld_q, const void* k_pages,
+// whether one of `tokens` rows of `row` bytes at a, ld_a bytes apart, shares a byte with one of those at b (slices of
+// one buffer may lie between one another)
+bool rows_overlap(const void* a, long long ld_a, const void* b, long long ld_b, long long row, long long tokens) {
+  const long long d = (long long)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)), n = tokens - 1;
+  if (tokens <= 0 || d >= n * ld_a + row || -d >= n * ld_b + row) return false;
+  // row j of b against the rows of a that begin before and after it; with one stride, row 0 of b against those of a
+  // on either side of it, were a to go on without end: any pair (i, j) with that difference i - j will do
+  const bool same = ld_a == ld_b;
+  for (long long j = 0; j <= (same ? 0 : n); ++j) {
+    const long long at = d + j * ld_b;
+    const long long i = at >= 0 ? at / ld_a : -((-at + ld_a - 1) / ld_a);
+    for (int k = 0; k < 2; ++k) {
+      const long long gap = at - (i + k) * ld_a;
+      if ((same ? i + k >= -n : i + k >= 0) && i + k <= n && gap < row && -gap < row) return true;
+    }
+  }
+  return false;
+}
+
+jamba_status check_attn_args(int n_heads, int tokens, const void* q, int ld_q, const void* k_pages,
                              const void* v_pages, const void* table, const void* lengths, const void* o, int ld_o,
                              const void* lse, const void* ws) {
   JB_TRY(check_ptr(q, "q"));
@@ -88,7 +107,8 @@ jamba_status check_attn_args(int n_heads, const void* q, int ld_q, const void* k
   const long long row = (long long)n_heads * PG_D;
   if (ld_q < row || ld_o < row || ld_q % 8 || ld_o % 8)
     return fail(JAMBA_ERR_INVALID_ARG, "paged attention: token strides must be multiples of 8 and hold all heads");
-  if (q == o) return fail(JAMBA_ERR_INVALID_ARG, "paged attention: o may not alias q");
+  if (q == o || rows_overlap(q, 2ll * ld_q, o, 2ll * ld_o, 2 * row, tokens))
+    return fail(JAMBA_ERR_INVALID_ARG, "paged attention: o may not overlap q");
   return JAMBA_OK;
 }
 
@@ -249,7 +269,7 @@ jamba_status jamba_paged_decode(const jamba_pages_config* cfg, int n_heads, cons
   PageGeom g;
   JB_TRY(geom(cfg, &g));
   JB_TRY(check_heads(g, n_heads, g.S, DECODE_MAX_REP));
-  JB_TRY(check_attn_args(n_heads, q, ld_q, k_pages, v_pages, table, lengths, o, ld_o, lse, ws));
+  JB_TRY(check_attn_args(n_heads, g.S, q, ld_q, k_pages, v_pages, table, lengths, o, ld_o, lse, ws));
   if (ws_bytes < paged_decode_workspace_bytes(g, n_heads))
     return fail(JAMBA_ERR_WORKSPACE, "paged decode: workspace too small");
   JB_TRY(ready());
@@ -266,7 +286,7 @@ jamba_status jamba_paged_extend(const jamba_pages_config* cfg, int n_heads, cons
   if (tokens < 0) return fail(JAMBA_ERR_INVALID_ARG, "paged extend: negative tokens");
   JB_TRY(check_heads(g, n_heads, tokens, EXTEND_MAX_REP));
   JB_TRY(check_int(q_start, "q_start"));
-  JB_TRY(check_attn_args(n_heads, q, ld_q, k_pages, v_pages, table, lengths, o, ld_o, lse, ws));
+  JB_TRY(check_attn_args(n_heads, tokens, q, ld_q, k_pages, v_pages, table, lengths, o, ld_o, lse, ws));
   if (ws_bytes < paged_extend_workspace_bytes())
     return fail(JAMBA_ERR_WORKSPACE, "paged extend: workspace too small");
   if (tokens == 0) return JAMBA_OK;

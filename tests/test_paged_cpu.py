@@ -155,3 +155,33 @@ def test_active_lengths_refuse_before_a_launch(lib):
     p, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 2)
     for args in ((0, p, p, p), ((1 << 20) + 1, p, p, p), (4, None, p, p), (4, p, odd, p), (4, p, p, None)):
         assert lib.jamba_pages_active(*args, None) == 1, args
+
+
+def test_outputs_that_overlap_queries_are_refused(lib):
+    """Views of one buffer: every pair of rows is compared by brute force; a call that does not overlap is
+    stopped by its workspace, before a launch."""
+    from mamba_selective_scan_mixer_b200 import _abi
+    base = 1 << 24
+    H = 2
+    row = H * 128                                        # elements
+    rng = np.random.default_rng(7)
+    seen = set()
+    for _ in range(3000):
+        T = int(rng.integers(1, 7))
+        ldq = int(rng.choice([row, row + 8, row + 64, 2 * row, 3 * row, 5 * row]))
+        ldo = ldq if rng.random() < 0.5 else int(rng.choice([row, row + 8, 2 * row, 4 * row]))
+        off = int(rng.integers(-6 * 5 * row // 8, 6 * 5 * row // 8)) * 8
+        if rng.random() < 0.5:
+            off = off // row * row
+        starts_q, starts_o = np.arange(T) * ldq, off + np.arange(T) * ldo
+        overlap = bool((np.abs(starts_q[:, None] - starts_o[None]) < row).any())
+        cfg = _abi.PagesConfig(64, 64, 2, 128, 2, T, 16, 16, _abi.JAMBA_BF16)
+        v = ctypes.c_void_p
+        q, o, p = v(base), v(base + 2 * off), v(1 << 20)
+        want = 1 if overlap else 3
+        st = lib.jamba_paged_decode(ctypes.byref(cfg), H, q, ldq, p, p, p, p, o, ldo, None, p, 0, None)
+        assert st == want, (T, ldq, ldo, off)
+        st = lib.jamba_paged_extend(ctypes.byref(cfg), H, q, ldq, T, p, p, p, p, p, o, ldo, None, p, 0, None)
+        assert st == want, (T, ldq, ldo, off)
+        seen.add((overlap, ldq == ldo))
+    assert len(seen) == 4
