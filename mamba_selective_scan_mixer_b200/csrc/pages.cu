@@ -15,6 +15,8 @@
 // a quarter of them copying a shared last page, 21 us; compaction that moves 0.51 GB 166 us, 0.94 of the
 // copy rate with its plan, in a pool of 160 pages 8 us; append of 33 prompts of 17 to 4001 tokens
 // 36 us, 0.89 of the copy rate, of one token for each of 64 sequences 4 us.
+#include <climits>
+
 #include "host.hpp"
 #include "pages.cuh"
 
@@ -23,22 +25,23 @@ namespace jb {
 constexpr int PLAN_THREADS = 1024;
 
 // Exclusive prefix sum over the CTA's PLAN_THREADS threads; `total` gets the sum.
-__device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int& total) {
+template <typename T>
+__device__ __forceinline__ T block_exclusive(T v, T* warp_sums, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();               // the last call's sums have been read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int w = warp_sums[lane];
+    T w = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      const T y = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += y;
     }
     warp_sums[lane] = w;
@@ -133,7 +136,7 @@ pages_fork_small_kernel(PageGeom g, const int* __restrict__ parent, int* refs, i
 
 struct GrowRecord {
   int len, add;      // tokens before, tokens to add
-  int first, end;    // ranks of the free pages wanted: first .. end - 1
+  int first, end;    // ranks of the free pages wanted: first .. end - 1 (INT_MAX: further than any pool)
   int src;           // page to copy the rows of (-1: none); its copy takes rank `first`
   int fits;          // 0: would pass max_pages
 };
@@ -145,9 +148,11 @@ pages_grow_plan_kernel(PageGeom g, const int* __restrict__ add, const int* __res
                        const int* __restrict__ table, const int* __restrict__ lengths, GrowRecord* __restrict__ rec,
                        int* __restrict__ free_list, int* __restrict__ copiers, int* __restrict__ counts, int* err) {
   __shared__ int sums[32];
+  __shared__ long long wide_sums[32];
   griddep_wait();
   griddep_launch();
-  int wanted = 0, copying = 0, total;
+  long long wanted = 0, wide_total;              // refused slots' pages count too: more than 2^31 in a large table
+  int copying = 0, total;
   for (int s0 = 0; s0 < g.S; s0 += PLAN_THREADS) {
     const int s = s0 + threadIdx.x;
     GrowRecord r = {};
@@ -169,11 +174,11 @@ pages_grow_plan_kernel(PageGeom g, const int* __restrict__ add, const int* __res
         }
       }
     }
-    const int at = block_exclusive(want, sums, total);
-    r.first = wanted + at;
-    r.end = r.first + want;
-    wanted += total;
-    const int c = block_exclusive(r.src >= 0, sums, total);
+    const long long at = wanted + block_exclusive((long long)want, wide_sums, wide_total);
+    r.first = (int)min(at, (long long)INT_MAX);
+    r.end = (int)min(at + want, (long long)INT_MAX);
+    wanted += wide_total;
+    const int c = block_exclusive((int)(r.src >= 0), sums, total);
     if (r.src >= 0) copiers[copying + c] = s;
     copying += total;
     if (s < g.S) rec[s] = r;

@@ -891,3 +891,17 @@ def test_free_in_a_graph(J):
         graph.replay()
         assert granted.tolist() == [1, 1, 1] and cache.lengths.tolist() == [20, 30, 5]
         assert int((cache.refs > 0).sum()) == 5 and int(cache.refs.sum()) == 5
+
+
+def test_grow_where_the_pages_wanted_pass_32_bits(J):
+    """65536 slots that want 32769 pages each, more than 2^31 in all, of a pool of 8: every one is refused, whatever
+    its rank, and slots that want one page or none are not, before them and after."""
+    S, W, P, N = 1 << 16, (1 << 15) + 1, 16, 8
+    table = torch.empty(S, W, dtype=torch.int32, device="cuda")      # 8.6 GB; a slot of length 0 holds no entry
+    lengths, refs = torch.zeros(S, dtype=torch.int32, device="cuda"), torch.zeros(N, dtype=torch.int32, device="cuda")
+    data = torch.zeros(2, N, 1, P, 128, dtype=BF, device="cuda")
+    add = torch.full((S,), W * P, dtype=torch.int32, device="cuda")
+    add[:3], add[S - 2:] = 10, 0
+    granted = J.pages_grow(add, data, refs, table, lengths)
+    assert (granted.nonzero()[:, 0].tolist() == [0, 1, 2, S - 2, S - 1]) and refs.tolist() == [1] * 3 + [0] * 5
+    assert lengths.nonzero()[:, 0].tolist() == [0, 1, 2] and table[:3, 0].tolist() == [0, 1, 2]
