@@ -62,7 +62,7 @@ struct ExSmem {
 
 struct ExMeta {                                  // of a CTA's first and last item
   int tail, s, g, u;                             // tail: the last item begins a unit that ends in another CTA
-  int head, ends;                                // head: the first item continues a unit; ends: and ends it
+  int ends;                                      // the first item ends its unit
 };
 
 struct ExParams {
@@ -629,16 +629,13 @@ paged_extend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     int ns = 0, no = 0;
     bool ok = true, first_item = true;
     const bool scribe = t == 0 && row0 == 0 && lane == 0;
-    if (scribe) p.meta[blockIdx.x].tail = p.meta[blockIdx.x].head = 0;
+    if (scribe) p.meta[blockIdx.x].tail = 0;
     for (bool more = w.open(p); more && ok; more = w.next(p), first_item = false) {
       const int nt = w.tokens_of(p, t);
       const bool whole = w.kb0 == 0 && w.kb1 == w.nb;
       if (scribe) {
         ExMeta* m = p.meta + blockIdx.x;
-        if (first_item) {
-          m->head = w.kb0 > 0;
-          m->ends = w.kb1 == w.nb;
-        }
+        if (first_item) m->ends = w.kb1 == w.nb;
         m->tail = w.kb0 == 0 && w.kb1 < w.nb;    // only the last item can be one
         m->s = w.s;
         m->g = w.g;
