@@ -23,9 +23,9 @@
 // product as a bf16 and the bf16 of what that left out: the tensor cores have time to spare, and the
 // output is then rounded once instead of twice.
 //
-// Measured: 64 sequences of 2048 tokens, 32 heads on 8, 89.5 us with the join, 6.0 TB/s, 0.92 of the
+// Measured: 64 sequences of 2048 tokens, 32 heads on 8, 89.8 us with the join, 6.0 TB/s, 0.91 of the
 // copy rate (one CTA per part with plain loads before it: 108.5 us); 24 sequences of 1 to 131072
-// tokens, 64 heads, pages of 16: 232 us, 0.93; one sequence of 200 tokens 7.6 us, two launches and
+// tokens, 64 heads, pages of 16: 235 us, 0.91; one sequence of 200 tokens 7.6 us, two launches and
 // the latency of four blocks.  Parts joined inside this kernel by the CTA that ends last took 91 to
 // 93 us at the first size (fences under full memory traffic).
 #include "host.hpp"

@@ -2,7 +2,7 @@
 //
 //   o_t = sum_j softmax_j(q_t . k_j / sqrt(d)) v_j over the positions j <= pos(t),
 //   lse_t = log sum_j exp(q_t . k_j / sqrt(d)),
-// in one pass over the keys with a running maximum and sum.
+// in one pass over the keys with a running reference and sum of the exponentials.
 //
 // Rows: the query heads of a KV head's group stand next to one another, row r of a tile is token
 // r / rep, head r % rep, so that one token with a wide group, a few drafted tokens and a long chunk
@@ -30,15 +30,15 @@
 // Rounding: P is bf16 (the tensor core's type; the sum is taken before), o is rounded once from fp32.
 //
 // Bounds: chunks by the tensor core and the softmax it waits for.  4096 tokens behind 12288, 32 heads
-// on 8: 0.87 ms, 1.1 PFLOP/s, 0.67 of the burst rate and 0.82 of the sustained one (the card holds
+// on 8: 0.885 ms, 1.09 PFLOP/s, 0.66 of the burst rate and 0.80 of the sustained one (the card holds
 // 1.55 to 1.65 GHz under it): a pair of blocks takes about 3600 cycles, its four products 2500 with
 // the shared memory's other traffic, the rest is the chain softmax (1600) -> products (1270) -> the
-// next wait.  Measured there: a maximum taken of every block and the reference raised from 2^8 on
-// 0.95 ms; before that without turns 1.07 ms; P handed over in halves 1.03 ms; 64-key blocks with two
-// score buffers a tile 1.18 ms; all 16 warps on one tile's softmax 1.20 ms.  24 sequences of 1 to 1500
-// tokens behind up to 6000: 0.142 ms (one warp issuing for both tiles 0.245 ms).  A few drafted
-// tokens (32 sequences of 5 behind 300 to 4096): 57 us, by the latency of a block, at half the rate
-// that reading their pages allows.  Every wait is bounded (see common.cuh).
+// next wait.  Measured there, when this form took 0.87 ms: a maximum taken of every block and the reference
+// raised from 2^8 on 0.95 ms; before that without turns 1.07 ms; P handed over in halves 1.03 ms; 64-key
+// blocks with two score buffers a tile 1.18 ms; all 16 warps on one tile's softmax 1.20 ms.  24 sequences
+// of 1 to 1500 tokens behind up to 6000: 0.146 ms (one warp issuing for both tiles 0.245 ms).  A few
+// drafted tokens (32 sequences of 5 behind 300 to 4096): 58 us, by the latency of a block, at half the
+// rate that reading their pages allows.  Every wait is bounded (see common.cuh).
 #include <climits>
 
 #include "host.hpp"
@@ -255,7 +255,7 @@ constexpr float EXC0 = 0.99999926144f, EXC1 = 0.69312181475f, EXC2 = 0.240247448
 // result, some 2^-126, is as good as none; above it and for a NaN it is at least 2^126, which the row's sum
 // shows.  Without the upper limit the exponent would run into the sign and a far key vanish.  Takes some of the
 // terms because ex2 alone runs at 16 a cycle and SM: 128 x 256 terms take the 2048 cycles that their
-// four products take.
+// four products take.  The upper limit costs 1.3 % of a chunk (873 to 884 us).
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
   const float big = 12582912.f;
   x.x = fminf(nan_max(x.x, -126.f), 127.f);      // a NaN becomes 127
